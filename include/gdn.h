@@ -454,6 +454,78 @@ GDN_API gdn_status gdn_frontend_decode_step(const void *q_raw, const void *k_raw
                                     float eps, void *q, void *k, void *v,
                                     float *log_alpha, float *beta, void *stream);
 
+/*
+ * The calls below take token-major tensors with a row stride: row t of a tensor
+ * starts at element t * stride, its columns are dense, and stride >= the row's
+ * columns -- so an input may be a column slice of a fused projection and an
+ * output a slice of its gradient.  Their data pointers need the alignment of
+ * their element type; 16-byte aligned pointers with row strides that are
+ * multiples of 16 bytes take the wide (vector or TMA) path, others a slower one
+ * with the same results up to the order of sums.  Outputs must not overlap
+ * inputs unless a call says so.
+ */
+
+typedef enum {
+    GDN_NORM_RMS = 0,  /* divide by the root of the mean square */
+    GDN_NORM_MEAN = 1  /* subtract the mean first (group norm) */
+} gdn_norm_kind;
+
+/* Most channels of one group of gdn_group_norm. */
+#define GDN_MAX_GROUP_DIM 1024
+
+/*
+ * gdn_group_norm -- the step behind the recurrence: normalise every head of a
+ * mixer's output (channels last, one group per token and head), scale it, and
+ * apply the activation or the activated gate.
+ *
+ *     m  = mean of the group (GDN_NORM_MEAN) or 0 (GDN_NORM_RMS)
+ *     xh = (x - m) / sqrt(mean of (x - m)^2 + eps)
+ *     n  = weight xh + bias
+ *     y  = n act(z)   with a gate z,   y = act(n)   without
+ *
+ * (The pages name an output norm and a gate around the mixers and print no
+ * formula.)
+ *
+ *   x, z, y   : [T, H, d] io_dtype; row strides over tokens, the H d columns of a
+ *               token dense; z NULL for no gate.  1 <= d <= GDN_MAX_GROUP_DIM.
+ *   weight    : fp32 [weight_heads, d], bias the same or NULL; weight_heads is 1
+ *               (shared by the heads) or H.
+ *   eps       : >= 0.
+ * Statistics and products are fp32; y is rounded once.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED (d out of range) or
+ * GDN_ERR_CUDA.
+ */
+GDN_API gdn_status gdn_group_norm(const void *x, int64_t x_stride, const void *z,
+                                  int64_t z_stride, const float *weight, const float *bias,
+                                  int32_t T, int32_t H, int32_t d, int32_t weight_heads,
+                                  gdn_norm_kind norm, gdn_activation act, float eps,
+                                  gdn_dtype io_dtype, void *y, int64_t y_stride, void *stream);
+
+/*
+ * gdn_group_norm_backward -- the gradients of <dy, y> for gdn_group_norm.  The
+ * statistics are recomputed from x: nothing is kept from the forward call.
+ *
+ *   dy        : [T, H, d] io_dtype; x, z, weight, bias as given to the forward.
+ *   dx, dz    : [T, H, d] io_dtype with row strides (written); dz exactly when z.
+ *   dweight   : fp32 [weight_heads, d] (written: zeros when T == 0); dbias the same,
+ *               or NULL to skip it.
+ *   workspace : at least gdn_group_norm_backward_workspace_size(...) bytes, 256-byte
+ *               aligned: partial sums of dweight and dbias, added in a fixed order.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE or
+ * GDN_ERR_CUDA.
+ */
+GDN_API gdn_status gdn_group_norm_backward(
+    const void *dy, int64_t dy_stride, const void *x, int64_t x_stride, const void *z,
+    int64_t z_stride, const float *weight, const float *bias, int32_t T, int32_t H, int32_t d,
+    int32_t weight_heads, gdn_norm_kind norm, gdn_activation act, float eps, gdn_dtype io_dtype,
+    void *dx, int64_t dx_stride, void *dz, int64_t dz_stride, float *dweight, float *dbias,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of gdn_group_norm_backward on the current device (0 when T == 0
+ * or the arguments are invalid). */
+GDN_API size_t gdn_group_norm_backward_workspace_size(int32_t T, int32_t H, int32_t d,
+                                                      int32_t weight_heads, gdn_dtype io_dtype);
+
 /* Static, human-readable name of a status code. */
 GDN_API const char *gdn_status_string(gdn_status status);
 

@@ -436,6 +436,108 @@ gdn_status gdn_frontend_decode_step(const void* q_raw, const void* k_raw, const 
     return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+// A token-major tensor of T rows of `cols` dense columns, rows `stride` elements apart.
+bool rows_ok(const void* p, int64_t stride, int64_t cols, int elem) {
+    return p && aligned(p, elem) && stride >= cols && stride < (1ll << 32);
+}
+
+int elem_bytes(gdn_dtype t) { return t == GDN_BF16 ? 2 : 4; }
+
+gdn_status check_group_norm(int32_t T, int32_t H, int32_t d, int32_t weight_heads,
+                            gdn_norm_kind norm, gdn_activation act, float eps, gdn_dtype dt) {
+    if (T < 0 || H <= 0 || d <= 0 || (weight_heads != 1 && weight_heads != H))
+        return GDN_ERR_INVALID_ARG;
+    if (dt != GDN_BF16 && dt != GDN_F32) return GDN_ERR_INVALID_ARG;
+    if ((norm != GDN_NORM_RMS && norm != GDN_NORM_MEAN) ||
+        (act != GDN_ACT_NONE && act != GDN_ACT_SILU) || !(eps >= 0.f))
+        return GDN_ERR_INVALID_ARG;
+    if (d > GDN_MAX_GROUP_DIM) return GDN_ERR_UNSUPPORTED;
+    if ((long long)H * d >= (1ll << 30) || (long long)T * H >= (1ll << 40))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_group_norm(const void* x, int64_t x_stride, const void* z, int64_t z_stride,
+                          const float* weight, const float* bias, int32_t T, int32_t H, int32_t d,
+                          int32_t weight_heads, gdn_norm_kind norm, gdn_activation act, float eps,
+                          gdn_dtype io_dtype, void* y, int64_t y_stride, void* stream) {
+    gdn_status st = check_group_norm(T, H, d, weight_heads, norm, act, eps, io_dtype);
+    if (st != GDN_OK) return st;
+    if (T == 0) return GDN_OK;
+    const int64_t cols = (int64_t)H * d;
+    const int e = elem_bytes(io_dtype);
+    if (!rows_ok(x, x_stride, cols, e) || !rows_ok(y, y_stride, cols, e) ||
+        (z && !rows_ok(z, z_stride, cols, e)) || !weight || !aligned(weight, 4) ||
+        !aligned(bias, 4))
+        return GDN_ERR_INVALID_ARG;
+    st = check_device();
+    if (st != GDN_OK) return st;
+    gdn::GroupNormArgs a{};
+    a.x = x, a.z = z, a.y = y, a.weight = weight, a.bias = bias;
+    a.x_stride = x_stride, a.z_stride = z_stride, a.y_stride = y_stride;
+    a.T = T, a.H = H, a.d = d, a.weight_heads = weight_heads;
+    a.centred = norm == GDN_NORM_MEAN, a.silu = act == GDN_ACT_SILU;
+    a.bf16 = io_dtype == GDN_BF16, a.eps = eps;
+    return gdn::launch_group_norm(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
+size_t gdn_group_norm_backward_workspace_size(int32_t T, int32_t H, int32_t d,
+                                              int32_t weight_heads, gdn_dtype io_dtype) {
+    if (check_group_norm(T, H, d, weight_heads, GDN_NORM_RMS, GDN_ACT_NONE, 0.f, io_dtype) !=
+        GDN_OK)
+        return 0;
+    return gdn::group_norm_backward_workspace_bytes(T, H, d, weight_heads, io_dtype == GDN_BF16);
+}
+
+gdn_status gdn_group_norm_backward(const void* dy, int64_t dy_stride, const void* x,
+                                   int64_t x_stride, const void* z, int64_t z_stride,
+                                   const float* weight, const float* bias, int32_t T, int32_t H,
+                                   int32_t d, int32_t weight_heads, gdn_norm_kind norm,
+                                   gdn_activation act, float eps, gdn_dtype io_dtype, void* dx,
+                                   int64_t dx_stride, void* dz, int64_t dz_stride, float* dweight,
+                                   float* dbias, void* workspace, size_t workspace_bytes,
+                                   void* stream) {
+    gdn_status st = check_group_norm(T, H, d, weight_heads, norm, act, eps, io_dtype);
+    if (st != GDN_OK) return st;
+    const int64_t cols = (int64_t)H * d;
+    const int e = elem_bytes(io_dtype);
+    if (!dweight || !aligned(dweight, 4) || !aligned(dbias, 4)) return GDN_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!rows_ok(dy, dy_stride, cols, e) || !rows_ok(x, x_stride, cols, e) ||
+            !rows_ok(dx, dx_stride, cols, e) || !weight || !aligned(weight, 4) ||
+            !aligned(bias, 4) || (z != nullptr) != (dz != nullptr))
+            return GDN_ERR_INVALID_ARG;
+        if (z && (!rows_ok(z, z_stride, cols, e) || !rows_ok(dz, dz_stride, cols, e)))
+            return GDN_ERR_INVALID_ARG;
+        if (!workspace || !aligned(workspace, 256) ||
+            workspace_bytes < gdn_group_norm_backward_workspace_size(T, H, d, weight_heads, io_dtype))
+            return GDN_ERR_WORKSPACE;
+    }
+    st = check_device();
+    if (st != GDN_OK) return st;
+    gdn::GroupNormArgs a{};
+    a.x = x, a.z = z, a.dy = dy, a.y = dx, a.dz = dz, a.weight = weight, a.bias = bias;
+    a.x_stride = x_stride, a.z_stride = z_stride, a.dy_stride = dy_stride;
+    a.y_stride = dx_stride, a.dz_stride = dz_stride;
+    a.T = T, a.H = H, a.d = d, a.weight_heads = weight_heads;
+    a.centred = norm == GDN_NORM_MEAN, a.silu = act == GDN_ACT_SILU;
+    a.bf16 = io_dtype == GDN_BF16, a.eps = eps;
+    return gdn::launch_group_norm_backward(a, dweight, dbias, workspace,
+                                           static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_selftest_bounded_wait(void* stream) {
     gdn_status st = check_device();
     if (st != GDN_OK) return st;

@@ -79,6 +79,21 @@ cudaError_t launch_frontend_decode(const void* q_raw, const void* k_raw, const v
                                    float eps, void* q, void* k, void* v, float* log_alpha,
                                    float* beta, cudaStream_t stream);
 
+// Group norm over heads (strides in elements; y is dx in the backward form).
+struct GroupNormArgs {
+    const void *x, *z, *dy;
+    void *y, *dz;
+    const float *weight, *bias;
+    int64_t x_stride, z_stride, dy_stride, y_stride, dz_stride;
+    int T, H, d, weight_heads;
+    bool centred, silu, bf16;
+    float eps;
+};
+cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream);
+size_t group_norm_backward_workspace_bytes(int T, int H, int d, int weight_heads, bool bf16);
+cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, float* dbias,
+                                       void* workspace, cudaStream_t stream);
+
 cudaError_t read_and_clear_status(unsigned int* status, cudaStream_t stream);
 
 // Fixed-size device scratch used by gdn_prefill_noalloc (bytes, and its address

@@ -7,6 +7,7 @@ fallback: if the library is missing, or a call fails, an exception is raised.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -26,6 +27,9 @@ GDN_F32 = 2
 GDN_ACT_NONE = 0
 GDN_ACT_SILU = 1
 _ACTS = {"none": GDN_ACT_NONE, "silu": GDN_ACT_SILU}
+GDN_NORM_RMS = 0
+GDN_NORM_MEAN = 1
+_NORMS = {"rms": GDN_NORM_RMS, "mean": GDN_NORM_MEAN}
 
 # Every exported symbol of include/gdn.h with its ctypes signature.
 _c = ctypes
@@ -73,6 +77,14 @@ SIGNATURES = {
                      [_c.c_void_p] * 6),
     "gdn_frontend_decode_step": (_c.c_int, [_c.c_void_p] * 7 + [_c.c_int32] * 5 +
                                  [_c.c_int, _c.c_int, _c.c_float] + [_c.c_void_p] * 6),
+    "gdn_group_norm": (_c.c_int, [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] * 2 +
+                       [_c.c_int32] * 4 + [_c.c_int, _c.c_int, _c.c_float, _c.c_int] +
+                       [_c.c_void_p, _c.c_int64, _c.c_void_p]),
+    "gdn_group_norm_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_void_p] * 2 +
+                                [_c.c_int32] * 4 + [_c.c_int, _c.c_int, _c.c_float, _c.c_int] +
+                                [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] * 3 +
+                                [_c.c_size_t, _c.c_void_p]),
+    "gdn_group_norm_backward_workspace_size": (_c.c_size_t, [_c.c_int32] * 4 + [_c.c_int]),
     "gdn_get_last_device_error": (_c.c_int, [_c.c_void_p]),
     "gdn_selftest_bounded_wait": (_c.c_int, [_c.c_void_p]),
     "gdn_status_string": (_c.c_char_p, [_c.c_int]),
@@ -417,6 +429,187 @@ def frontend_decode_step(q_raw, k_raw, v_raw, conv_w, a, b, conv_state, *, act="
     if st != GDN_OK:
         raise GDNError(st, "gdn_frontend_decode_step")
     return q, k, v, la, be
+
+
+_DTYPES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+
+
+def _choice(value, choices, name):
+    got = choices.get(value)
+    if got is None:
+        raise ValueError(f"{name}: one of {', '.join(map(repr, choices))}, not {value!r}")
+    return got
+
+
+def _dtype_of(t, name):
+    got = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
+    if got is None:
+        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
+    return got
+
+
+def _rows(t, name, dtype, shape, device) -> int:
+    """Row stride of a token-major tensor whose rows are dense (a column slice of a wider
+    tensor will do); raises where it is not of this dtype, shape and device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    cols = 1
+    for i in range(len(shape) - 1, 0, -1):
+        if shape[i] != 1 and t.stride(i) != cols:
+            raise ValueError(f"the rows of {name} must be dense, got strides {t.stride()}")
+        cols *= shape[i]
+    if shape[0] <= 1:
+        return cols
+    if t.stride(0) < cols:
+        raise ValueError(f"the rows of {name} overlap: strides {t.stride()}")
+    return t.stride(0)
+
+
+def _dense(t, name, dtype, shape, device):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _placed(fn):
+    """Run ``fn`` on the device of its first argument and on ``stream`` (None: that device's
+    current stream), outputs and workspaces allocated there too.  With a ``stream`` of its
+    own, every tensor given is kept from reuse until the work on that stream is done."""
+
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+        device = first.device
+        if stream is None:
+            if device.index == torch.cuda.current_device():
+                return fn(first, *args, **kw)
+            with torch.cuda.device(device):
+                return fn(first, *args, **kw)
+        if stream.device != device:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
+                             f"{device}")
+        # (a stream's context makes its device current as well)
+        with torch.cuda.stream(stream):
+            out = fn(first, *args, **kw)
+        given = [first, *args, *kw.values()]
+        while given:
+            t = given.pop()
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
+            elif isinstance(t, (tuple, list)):
+                given.extend(t)
+        return out
+
+    return call
+
+
+def _here(device):
+    """The current stream of a device, as a cudaStream_t."""
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
+    _dense(workspace, "workspace", workspace.dtype, workspace.shape, device)
+    return workspace
+
+
+def _nbytes(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def _norm_args(x, weight, bias, z):
+    if x.dim() != 3:
+        raise ValueError(f"x must be [T, H, d], got {tuple(x.shape)}")
+    io = _dtype_of(x, "x")
+    T, H, d = x.shape
+    dev = x.device
+    shared = (d,)
+    if not isinstance(weight, torch.Tensor) or weight.shape not in (shared, (H, d)):
+        raise ValueError(f"weight must have shape ({d},) or ({H}, {d})")
+    _dense(weight, "weight", torch.float32, weight.shape, dev)
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, weight.shape, dev)
+    return (T, H, d, 1 if weight.dim() == 1 else H, io, _rows(x, "x", x.dtype, x.shape, dev),
+            0 if z is None else _rows(z, "z", x.dtype, x.shape, dev))
+
+
+@_placed
+def group_norm(x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6, y=None):
+    """Norm over every head of a mixer's output, with its activation or activated gate
+    (gdn_group_norm): ``y = n act(z)`` with a gate ``z``, ``act(n)`` without, where
+    ``n = weight xh + bias`` and ``xh`` is x [T, H, d] normalised over d -- ``norm`` "rms"
+    or "mean" (centred).  ``weight`` and ``bias``: fp32 [d] or [H, d].  x, z and y may be
+    column slices of wider tensors.  Returns ``y`` in x's type.  ``stream``: as for the
+    other calls."""
+    T, H, d, wh, io, xs, zs = _norm_args(x, weight, bias, z)
+    if y is None:
+        y = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
+    ys = _rows(y, "y", x.dtype, x.shape, x.device)
+    st = lib().gdn_group_norm(x.data_ptr(), xs, _at(z), zs, weight.data_ptr(), _at(bias), T, H, d,
+                              wh, _choice(norm, _NORMS, "norm"), _choice(act, _ACTS, "act"), eps,
+                              io, y.data_ptr(), ys, _here(x.device))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_group_norm")
+    return y
+
+
+@_placed
+def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6,
+                        dx=None, dz=None, workspace=None):
+    """Gradients of ``<dy, y>`` for :func:`group_norm` (gdn_group_norm_backward).
+
+    Returns ``(dx, dweight, dbias, dz)``: dx and dz in x's type, dweight and dbias fp32 of
+    weight's shape; dbias None without a bias, dz None without a gate.  ``dx`` and ``dz``
+    may be given (column slices of wider tensors will do)."""
+    T, H, d, wh, io, xs, zs = _norm_args(x, weight, bias, z)
+    dev = x.device
+    dys = _rows(dy, "dy", x.dtype, x.shape, dev)
+    if dx is None:
+        dx = torch.empty((T, H, d), dtype=x.dtype, device=dev)
+    dxs = _rows(dx, "dx", x.dtype, x.shape, dev)
+    if z is None and dz is not None:
+        raise ValueError("dz without z")
+    dzs = 0
+    if z is not None:
+        if dz is None:
+            dz = torch.empty((T, H, d), dtype=x.dtype, device=dev)
+        dzs = _rows(dz, "dz", x.dtype, x.shape, dev)
+    dw = torch.empty_like(weight, requires_grad=False)
+    db = None if bias is None else torch.empty_like(weight, requires_grad=False)
+    L = lib()
+    if workspace is None:
+        need = L.gdn_group_norm_backward_workspace_size(T, H, d, wh, io)
+        workspace = _workspace(None, need, dev)
+    else:
+        _workspace(workspace, 0, dev)
+    st = L.gdn_group_norm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _at(z), zs,
+                                   weight.data_ptr(), _at(bias), T, H, d, wh,
+                                   _choice(norm, _NORMS, "norm"), _choice(act, _ACTS, "act"), eps,
+                                   io, dx.data_ptr(), dxs, _at(dz), dzs, dw.data_ptr(), _at(db),
+                                   _at(workspace), _nbytes(workspace), _here(dev))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_group_norm_backward")
+    return dx, dw, db, dz
 
 
 def selftest_bounded_wait(stream=None) -> None:
