@@ -465,6 +465,79 @@ GDN_API gdn_status gdn_frontend_decode_step(const void *q_raw, const void *k_raw
  * inputs unless a call says so.
  */
 
+/*
+ * gdn_scan -- the gated linear recurrence, per channel, over N packed sequences:
+ *
+ *     h_t = exp(log_alpha_t) h_{t-1} + x_t
+ *
+ * the elementwise mixer beside the matrix-valued gated delta rule of
+ * gdn_prefill: a state of one number per channel, and a gate of its own for
+ * every channel and token.  (The pages describe the delta rule alone; the
+ * formula here is the recurrence's own definition.)
+ *
+ *   x         : [T, C] io_dtype, row stride x_stride.
+ *   log_alpha : [T, C] gate_dtype, row stride la_stride.  <= 0 in normal use; -inf
+ *               is a gate of 0.  Larger values are allowed as long as every
+ *               product of consecutive gates stays within fp32.
+ *   h0        : [N, C] fp32, the state before each sequence, or NULL for zeros.
+ *   cu_seqlens: device int32 [N+1] as for gdn_prefill, or NULL for one sequence
+ *               of T tokens (N = 1).  Here cu[N] may be below T: the rows of
+ *               padding from cu[N] on are neither used nor written.
+ *   h         : [T, C] io_dtype, row stride h_stride (written).
+ *   h_final   : [N, C] fp32, the state after each sequence (h0 or 0 for an empty
+ *               one), or NULL to skip it.  May alias h0 exactly.
+ *
+ * The recurrence runs in fp32 and h is rounded once.  No value crosses from one
+ * sequence into another, not even an infinity or a NaN.  The result does not
+ * depend on timing: the same call gives the same bits.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API gdn_status gdn_scan(const void *x, int64_t x_stride, const void *log_alpha,
+                            int64_t la_stride, const float *h0, const int32_t *cu_seqlens,
+                            int32_t N, int32_t T, int32_t C, gdn_dtype io_dtype,
+                            gdn_dtype gate_dtype, void *h, int64_t h_stride, float *h_final,
+                            void *stream);
+
+/*
+ * gdn_scan_backward -- the gradients of L = <dh, h> + <dh_final, h_final> for
+ * gdn_scan, by the chain rule of its recurrence: with g_t = dL/dh_t in full,
+ *
+ *     g_t = dh_t + exp(log_alpha_{t+1}) g_{t+1}      (the last token: dh_t + dh_final)
+ *     dx_t = g_t,  dlog_alpha_t = g_t exp(log_alpha_t) h_{t-1},  dh0 = exp(log_alpha) g at
+ *     the first token.
+ *
+ *   log_alpha, h0, cu_seqlens, N, T, C: gdn_scan's (h0 may be NULL).
+ *   h         : [T, C] io_dtype, gdn_scan's output; h_{t-1} is read from it, so
+ *               for GDN_BF16 dlog_alpha carries its rounding.
+ *   dh        : [T, C] io_dtype, the gradient of h.
+ *   dh_final  : [N, C] fp32, the gradient of h_final, or NULL for zeros.
+ *   dx        : [T, C] io_dtype (written); dlog_alpha: [T, C] gate_dtype (written).
+ *   dh0       : [N, C] fp32 (written; dh_final or 0 for an empty sequence), or
+ *               NULL to skip it.  May alias dh_final exactly.
+ * Rows from cu[N] on are neither used nor written.  Results and errors otherwise
+ * as for gdn_scan.
+ */
+GDN_API gdn_status gdn_scan_backward(const void *log_alpha, int64_t la_stride, const void *h,
+                                     int64_t h_stride, const void *dh, int64_t dh_stride,
+                                     const float *h0, const float *dh_final,
+                                     const int32_t *cu_seqlens, int32_t N, int32_t T, int32_t C,
+                                     gdn_dtype io_dtype, gdn_dtype gate_dtype, void *dx,
+                                     int64_t dx_stride, void *dlog_alpha, int64_t dla_stride,
+                                     float *dh0, void *stream);
+
+/*
+ * gdn_scan_step -- gdn_scan for one new token of each of B sequences:
+ * state = exp(log_alpha) state + x in place, h = state.
+ *
+ *   x, h [B, C] io_dtype, log_alpha [B, C] gate_dtype, with row strides;
+ *   state [B, C] fp32, dense: read, then overwritten.
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
+ */
+GDN_API gdn_status gdn_scan_step(const void *x, int64_t x_stride, const void *log_alpha,
+                                 int64_t la_stride, float *state, int32_t B, int32_t C,
+                                 gdn_dtype io_dtype, gdn_dtype gate_dtype, void *h,
+                                 int64_t h_stride, void *stream);
+
 typedef enum {
     GDN_NORM_RMS = 0,  /* divide by the root of the mean square */
     GDN_NORM_MEAN = 1  /* subtract the mean first (group norm) */

@@ -447,6 +447,17 @@ bool rows_ok(const void* p, int64_t stride, int64_t cols, int elem) {
 
 int elem_bytes(gdn_dtype t) { return t == GDN_BF16 ? 2 : 4; }
 
+gdn_status check_scan(const int32_t* cu_seqlens, int32_t N, int32_t T, int32_t C, gdn_dtype io,
+                      gdn_dtype gate) {
+    if (N <= 0 || T < 0 || C <= 0 || T > (1 << 30) || C > (1 << 22)) return GDN_ERR_INVALID_ARG;
+    if ((io != GDN_BF16 && io != GDN_F32) || (gate != GDN_BF16 && gate != GDN_F32))
+        return GDN_ERR_INVALID_ARG;
+    if ((long long)T * C >= (1ll << 40) || (long long)N * C >= (1ll << 40))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned(cu_seqlens, 4) || (!cu_seqlens && N != 1)) return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
 gdn_status check_group_norm(int32_t T, int32_t H, int32_t d, int32_t weight_heads,
                             gdn_norm_kind norm, gdn_activation act, float eps, gdn_dtype dt) {
     if (T < 0 || H <= 0 || d <= 0 || (weight_heads != 1 && weight_heads != H))
@@ -464,6 +475,73 @@ gdn_status check_group_norm(int32_t T, int32_t H, int32_t d, int32_t weight_head
 }  // namespace
 
 extern "C" {
+
+gdn_status gdn_scan(const void* x, int64_t x_stride, const void* log_alpha, int64_t la_stride,
+                    const float* h0, const int32_t* cu_seqlens, int32_t N, int32_t T, int32_t C,
+                    gdn_dtype io_dtype, gdn_dtype gate_dtype, void* h, int64_t h_stride,
+                    float* h_final, void* stream) {
+    gdn_status st = check_scan(cu_seqlens, N, T, C, io_dtype, gate_dtype);
+    if (st != GDN_OK) return st;
+    if (!aligned(h0, 4) || !aligned(h_final, 4)) return GDN_ERR_INVALID_ARG;
+    if (T > 0 && (!rows_ok(x, x_stride, C, elem_bytes(io_dtype)) ||
+                  !rows_ok(log_alpha, la_stride, C, elem_bytes(gate_dtype)) ||
+                  !rows_ok(h, h_stride, C, elem_bytes(io_dtype))))
+        return GDN_ERR_INVALID_ARG;
+    st = check_device();
+    if (st != GDN_OK) return st;
+    const gdn::ScanArgs a{x, log_alpha, h0, cu_seqlens, h, h_final, x_stride, la_stride, h_stride,
+                          N, T, C};
+    return gdn::launch_scan(a, io_dtype == GDN_BF16, gate_dtype == GDN_BF16,
+                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_scan_backward(const void* log_alpha, int64_t la_stride, const void* h,
+                             int64_t h_stride, const void* dh, int64_t dh_stride, const float* h0,
+                             const float* dh_final, const int32_t* cu_seqlens, int32_t N,
+                             int32_t T, int32_t C, gdn_dtype io_dtype, gdn_dtype gate_dtype,
+                             void* dx, int64_t dx_stride, void* dlog_alpha, int64_t dla_stride,
+                             float* dh0, void* stream) {
+    gdn_status st = check_scan(cu_seqlens, N, T, C, io_dtype, gate_dtype);
+    if (st != GDN_OK) return st;
+    if (!aligned(h0, 4) || !aligned(dh_final, 4) || !aligned(dh0, 4)) return GDN_ERR_INVALID_ARG;
+    const int e = elem_bytes(io_dtype), ge = elem_bytes(gate_dtype);
+    if (T > 0 && (!rows_ok(log_alpha, la_stride, C, ge) || !rows_ok(h, h_stride, C, e) ||
+                  !rows_ok(dh, dh_stride, C, e) || !rows_ok(dx, dx_stride, C, e) ||
+                  !rows_ok(dlog_alpha, dla_stride, C, ge)))
+        return GDN_ERR_INVALID_ARG;
+    st = check_device();
+    if (st != GDN_OK) return st;
+    const gdn::ScanGradArgs a{log_alpha, h, dh, h0, dh_final, cu_seqlens, dx, dlog_alpha, dh0,
+                              la_stride, h_stride, dh_stride, dx_stride, dla_stride, N, T, C};
+    return gdn::launch_scan_backward(a, io_dtype == GDN_BF16, gate_dtype == GDN_BF16,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
+gdn_status gdn_scan_step(const void* x, int64_t x_stride, const void* log_alpha,
+                         int64_t la_stride, float* state, int32_t B, int32_t C,
+                         gdn_dtype io_dtype, gdn_dtype gate_dtype, void* h, int64_t h_stride,
+                         void* stream) {
+    if (B < 0) return GDN_ERR_INVALID_ARG;
+    gdn_status st = check_scan(nullptr, 1, B, C, io_dtype, gate_dtype);
+    if (st != GDN_OK) return st;
+    if (B == 0) return GDN_OK;
+    if (!rows_ok(x, x_stride, C, elem_bytes(io_dtype)) ||
+        !rows_ok(log_alpha, la_stride, C, elem_bytes(gate_dtype)) ||
+        !rows_ok(h, h_stride, C, elem_bytes(io_dtype)) || !state || !aligned(state, 4))
+        return GDN_ERR_INVALID_ARG;
+    st = check_device();
+    if (st != GDN_OK) return st;
+    const gdn::ScanArgs a{x, log_alpha, nullptr, nullptr, h, state, x_stride, la_stride, h_stride,
+                          1, B, C};
+    return gdn::launch_scan_step(a, io_dtype == GDN_BF16, gate_dtype == GDN_BF16,
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
 
 gdn_status gdn_group_norm(const void* x, int64_t x_stride, const void* z, int64_t z_stride,
                           const float* weight, const float* bias, int32_t T, int32_t H, int32_t d,

@@ -79,6 +79,31 @@ cudaError_t launch_frontend_decode(const void* q_raw, const void* k_raw, const v
                                    float eps, void* q, void* k, void* v, float* log_alpha,
                                    float* beta, cudaStream_t stream);
 
+// The per-channel recurrence (row strides in elements; the step's T is its B and
+// its h_final the state).
+struct ScanArgs {
+    const void *x, *la;
+    const float* h0;
+    const int32_t* cu_seqlens;
+    void* h;
+    float* h_final;
+    int64_t x_stride, la_stride, h_stride;
+    int N, T, C;
+};
+struct ScanGradArgs {
+    const void *la, *h, *dh;
+    const float *h0, *dh_final;
+    const int32_t* cu_seqlens;
+    void *dx, *dla;
+    float* dh0;
+    int64_t la_stride, h_stride, dh_stride, dx_stride, dla_stride;
+    int N, T, C;
+};
+cudaError_t launch_scan(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream_t stream);
+cudaError_t launch_scan_backward(const ScanGradArgs& a, bool bf16, bool gate_bf16,
+                                 cudaStream_t stream);
+cudaError_t launch_scan_step(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream_t stream);
+
 // Group norm over heads (strides in elements; y is dx in the backward form).
 struct GroupNormArgs {
     const void *x, *z, *dy;

@@ -77,6 +77,14 @@ SIGNATURES = {
                      [_c.c_void_p] * 6),
     "gdn_frontend_decode_step": (_c.c_int, [_c.c_void_p] * 7 + [_c.c_int32] * 5 +
                                  [_c.c_int, _c.c_int, _c.c_float] + [_c.c_void_p] * 6),
+    "gdn_scan": (_c.c_int, [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] * 2 + [_c.c_int32] * 3 +
+                 [_c.c_int] * 2 + [_c.c_void_p, _c.c_int64] + [_c.c_void_p] * 2),
+    "gdn_scan_backward": (_c.c_int, [_c.c_void_p, _c.c_int64] * 3 + [_c.c_void_p] * 3 +
+                          [_c.c_int32] * 3 + [_c.c_int] * 2 + [_c.c_void_p, _c.c_int64] * 2 +
+                          [_c.c_void_p] * 2),
+    "gdn_scan_step": (_c.c_int, [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] +
+                      [_c.c_int32] * 2 + [_c.c_int] * 2 +
+                      [_c.c_void_p, _c.c_int64, _c.c_void_p]),
     "gdn_group_norm": (_c.c_int, [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] * 2 +
                        [_c.c_int32] * 4 + [_c.c_int, _c.c_int, _c.c_float, _c.c_int] +
                        [_c.c_void_p, _c.c_int64, _c.c_void_p]),
@@ -535,6 +543,103 @@ def _workspace(workspace, need, device):
 
 def _nbytes(t):
     return 0 if t is None else t.numel() * t.element_size()
+
+
+def _scan_sizes(first, cu_seqlens, device):
+    """(T, C, the shape of a token's channels, N, pointer of cu_seqlens)."""
+    if first.dim() < 2:
+        raise ValueError(f"expected [T, ...channels], got {tuple(first.shape)}")
+    T, chans = first.shape[0], first.shape[1:]
+    if cu_seqlens is None:
+        return T, chans.numel(), chans, 1, None
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
+    return T, chans.numel(), chans, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+
+
+@_placed
+def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_state=True):
+    """The gated linear recurrence ``h_t = exp(log_alpha_t) h_{t-1} + x_t`` per channel over
+    packed sequences (gdn_scan).
+
+    x [T, C] (or [T, H, d]: the channels may have several dimensions) bf16 or fp32, log_alpha
+    of the same shape, bf16 or fp32; ``h0`` [N, C] fp32 or None for zeros; ``cu_seqlens`` int32
+    [N + 1] on the device or None for one sequence.  x, log_alpha and h may be column slices
+    of wider tensors.  Returns ``(h, h_final)``: h in x's type, h_final [N, C] fp32 (None if
+    not wanted).  Rows from ``cu_seqlens[-1]`` on stay unwritten.  ``stream``: as for the
+    other calls."""
+    io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
+    T, C, chans, N, cu = _scan_sizes(x, cu_seqlens, dev)
+    xs = _rows(x, "x", x.dtype, shape, dev)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
+    if h0 is not None:
+        _dense(h0, "h0", torch.float32, (N, *chans), dev)
+    if h is None:
+        h, hs = torch.empty(shape, dtype=x.dtype, device=dev), C
+    else:
+        hs = _rows(h, "h", x.dtype, shape, dev)
+    if h_final is not None:
+        _dense(h_final, "h_final", torch.float32, (N, *chans), dev)
+    elif want_state:
+        h_final = torch.empty((N, *chans), dtype=torch.float32, device=dev)
+    st = lib().gdn_scan(x.data_ptr(), xs, log_alpha.data_ptr(), las, _at(h0), cu, N, T, C, io, gate,
+                        h.data_ptr(), hs, _at(h_final), _here(dev))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_scan")
+    return h, h_final
+
+
+@_placed
+def scan_backward(log_alpha, h, dh, h0=None, dh_final=None, cu_seqlens=None, *, dx=None,
+                  dlog_alpha=None, want_dh0=True):
+    """Gradients of ``<dh, h> + <dh_final, h_final>`` for :func:`scan` (gdn_scan_backward);
+    ``h`` is the scan's output.
+
+    Returns ``(dx, dlog_alpha, dh0)``: dx in h's type, dlog_alpha in log_alpha's, dh0 [N, C]
+    fp32 (None if not wanted)."""
+    io, gate, dev, shape = _dtype_of(h, "h"), _dtype_of(log_alpha, "log_alpha"), h.device, h.shape
+    T, C, chans, N, cu = _scan_sizes(h, cu_seqlens, dev)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
+    hs, dhs = _rows(h, "h", h.dtype, shape, dev), _rows(dh, "dh", h.dtype, shape, dev)
+    for t, name in ((h0, "h0"), (dh_final, "dh_final")):
+        if t is not None:
+            _dense(t, name, torch.float32, (N, *chans), dev)
+    if dx is None:
+        dx, dxs = torch.empty(shape, dtype=h.dtype, device=dev), C
+    else:
+        dxs = _rows(dx, "dx", h.dtype, shape, dev)
+    if dlog_alpha is None:
+        dlog_alpha, dlas = torch.empty(shape, dtype=log_alpha.dtype, device=dev), C
+    else:
+        dlas = _rows(dlog_alpha, "dlog_alpha", log_alpha.dtype, shape, dev)
+    dh0 = torch.empty((N, *chans), dtype=torch.float32, device=dev) if want_dh0 else None
+    st = lib().gdn_scan_backward(log_alpha.data_ptr(), las, h.data_ptr(), hs, dh.data_ptr(), dhs,
+                                 _at(h0), _at(dh_final), cu, N, T, C, io, gate, dx.data_ptr(), dxs,
+                                 dlog_alpha.data_ptr(), dlas, _at(dh0), _here(dev))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_scan_backward")
+    return dx, dlog_alpha, dh0
+
+
+@_placed
+def scan_step(x, log_alpha, state, *, h=None):
+    """One token of each of B sequences (gdn_scan_step): ``state`` [B, C] fp32 is updated in
+    place to ``exp(log_alpha) state + x``.  Returns ``h``, the new state in x's type."""
+    io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
+    B, C, _, _, _ = _scan_sizes(x, None, dev)
+    xs = _rows(x, "x", x.dtype, shape, dev)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
+    _dense(state, "state", torch.float32, shape, dev)
+    if h is None:
+        h, hs = torch.empty(shape, dtype=x.dtype, device=dev), C
+    else:
+        hs = _rows(h, "h", x.dtype, shape, dev)
+    st = lib().gdn_scan_step(x.data_ptr(), xs, log_alpha.data_ptr(), las, state.data_ptr(), B, C,
+                             io, gate, h.data_ptr(), hs, _here(dev))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_scan_step")
+    return h
 
 
 def _norm_args(x, weight, bias, z):
