@@ -599,6 +599,44 @@ GDN_API gdn_status gdn_group_norm_backward(
 GDN_API size_t gdn_group_norm_backward_workspace_size(int32_t T, int32_t H, int32_t d,
                                                       int32_t weight_heads, gdn_dtype io_dtype);
 
+/*
+ * gdn_frontend_backward -- the gradients of gdn_frontend: from those of q, k, v,
+ * log_alpha and beta to those of the raw projections, the convolution weight
+ * and the gates' pre-activations.  With u = act(y) of the convolution's y and
+ * r = 1 / sqrt(sum of u^2 + eps) per q or k head:
+ *
+ *     du = r (dq - q <q, dq>)  (v: dv),  dy = du act'(y)
+ *     dx[s]  = sum_i conv_w[., i] dy[s + 3 - i],  dconv_w[., i] = sum_t dy[t] x[t - 3 + i]
+ *     da = -sigmoid(a) dlog_alpha,  db = beta (1 - beta) dbeta
+ *
+ * every sum within its sequence.  y and u are recomputed from the raw inputs.
+ *
+ *   q_raw .. cu_seqlens, N .. eps : as given to gdn_frontend; cu_seqlens may be NULL
+ *               for one sequence of T tokens (N = 1), and cu[N] may be below T: the
+ *               rows from cu[N] on are neither used nor written.
+ *   dq, dk, dv  : gradients of q, k, v, their shapes and dtype; dlog_alpha, dbeta fp32.
+ *   dq_raw, dk_raw, dv_raw : io_dtype (written); da, db [T, H_v] fp32 (written).
+ *   dconv_w   : fp32 [(2 H_qk + H_v) * 128, 4] (written: zeros when T == 0).
+ *   workspace : at least gdn_frontend_backward_workspace_size(...) bytes, 256-byte
+ *               aligned: partial sums of dconv_w, added in a fixed order.
+ * Alignment as for gdn_frontend (dconv_w 16 bytes).
+ * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_WORKSPACE or
+ * GDN_ERR_CUDA.
+ */
+GDN_API gdn_status gdn_frontend_backward(
+    const void *q_raw, const void *k_raw, const void *v_raw, const float *conv_w, const float *a,
+    const float *b, const int32_t *cu_seqlens, const void *dq, const void *dk, const void *dv,
+    const float *dlog_alpha, const float *dbeta, int32_t N, int32_t T, int32_t H_qk, int32_t H_v,
+    int32_t head_dk, int32_t head_dv, gdn_dtype io_dtype, gdn_activation act, float eps,
+    void *dq_raw, void *dk_raw, void *dv_raw, float *dconv_w, float *da, float *db,
+    void *workspace, size_t workspace_bytes, void *stream);
+
+/* Workspace bytes of gdn_frontend_backward on the current device (0 when T == 0 or
+ * the arguments are invalid). */
+GDN_API size_t gdn_frontend_backward_workspace_size(int32_t T, int32_t H_qk, int32_t H_v,
+                                                    int32_t head_dk, int32_t head_dv,
+                                                    gdn_dtype io_dtype);
+
 /* Static, human-readable name of a status code. */
 GDN_API const char *gdn_status_string(gdn_status status);
 

@@ -447,6 +447,17 @@ bool rows_ok(const void* p, int64_t stride, int64_t cols, int elem) {
 
 int elem_bytes(gdn_dtype t) { return t == GDN_BF16 ? 2 : 4; }
 
+// T above 2^30 would leave no room for a run's three tokens ahead in 32 bits.
+gdn_status check_frontend_sizes(int32_t T, int32_t H_qk, int32_t H_v, int32_t dk, int32_t dv,
+                                gdn_dtype io) {
+    const gdn_status st = check_heads(H_qk, H_v, dk, dv, io);
+    if (st != GDN_OK) return st;
+    if (T < 0 || T > (1 << 30) || (2ll * H_qk + H_v) * kHeadDim * 4 > 0x7fffffffll ||
+        (long long)T * H_v * kHeadDim >= (1ll << 40))
+        return GDN_ERR_INVALID_ARG;
+    return GDN_OK;
+}
+
 gdn_status check_scan(const int32_t* cu_seqlens, int32_t N, int32_t T, int32_t C, gdn_dtype io,
                       gdn_dtype gate) {
     if (N <= 0 || T < 0 || C <= 0 || T > (1 << 30) || C > (1 << 22)) return GDN_ERR_INVALID_ARG;
@@ -612,6 +623,50 @@ gdn_status gdn_group_norm_backward(const void* dy, int64_t dy_stride, const void
     a.bf16 = io_dtype == GDN_BF16, a.eps = eps;
     return gdn::launch_group_norm_backward(a, dweight, dbias, workspace,
                                            static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GDN_OK
+               : GDN_ERR_CUDA;
+}
+
+size_t gdn_frontend_backward_workspace_size(int32_t T, int32_t H_qk, int32_t H_v, int32_t head_dk,
+                                            int32_t head_dv, gdn_dtype io_dtype) {
+    if (check_frontend_sizes(T, H_qk, H_v, head_dk, head_dv, io_dtype) != GDN_OK)
+        return 0;
+    return gdn::frontend_backward_workspace_bytes(T, H_qk, H_v);
+}
+
+gdn_status gdn_frontend_backward(const void* q_raw, const void* k_raw, const void* v_raw,
+                                 const float* conv_w, const float* a, const float* b,
+                                 const int32_t* cu_seqlens, const void* dq, const void* dk,
+                                 const void* dv, const float* dlog_alpha, const float* dbeta,
+                                 int32_t N, int32_t T, int32_t H_qk, int32_t H_v, int32_t head_dk,
+                                 int32_t head_dv, gdn_dtype io_dtype, gdn_activation act,
+                                 float eps, void* dq_raw, void* dk_raw, void* dv_raw,
+                                 float* dconv_w, float* da, float* db, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+    gdn_status st = check_frontend_sizes(T, H_qk, H_v, head_dk, head_dv, io_dtype);
+    if (st != GDN_OK) return st;
+    if (N <= 0 || (act != GDN_ACT_NONE && act != GDN_ACT_SILU) || !(eps >= 0.f))
+        return GDN_ERR_INVALID_ARG;
+    if (!aligned(cu_seqlens, 4) || (!cu_seqlens && N != 1)) return GDN_ERR_INVALID_ARG;
+    if (!dconv_w || !aligned(dconv_w, 16)) return GDN_ERR_INVALID_ARG;
+    if (T > 0) {
+        const void* p16[] = {q_raw, k_raw, v_raw, conv_w, dq, dk, dv, dq_raw, dk_raw, dv_raw};
+        for (const void* ptr : p16)
+            if (!ptr || !aligned(ptr, 16)) return GDN_ERR_INVALID_ARG;
+        const void* p4[] = {a, b, dlog_alpha, dbeta, da, db};
+        for (const void* ptr : p4)
+            if (!ptr || !aligned(ptr, 4)) return GDN_ERR_INVALID_ARG;
+        if (!workspace || !aligned(workspace, 256) ||
+            workspace_bytes < gdn::frontend_backward_workspace_bytes(T, H_qk, H_v))
+            return GDN_ERR_WORKSPACE;
+    }
+    st = check_device();
+    if (st != GDN_OK) return st;
+    const gdn::FrontendGradArgs g{{q_raw, k_raw, v_raw}, {dq, dk, dv}, {dq_raw, dk_raw, dv_raw},
+                                  conv_w, a, b, dlog_alpha, dbeta, dconv_w, da, db, cu_seqlens,
+                                  N, T, H_qk, H_v, io_dtype == GDN_BF16, act == GDN_ACT_SILU, eps};
+    return gdn::launch_frontend_backward(g, workspace, static_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? GDN_OK
                : GDN_ERR_CUDA;
 }

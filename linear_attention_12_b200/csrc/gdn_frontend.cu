@@ -306,7 +306,206 @@ __global__ void __launch_bounds__(32)
     }
 }
 
+// ---- gradients of the front end ----
+//
+// With y the convolution, u = act(y) and r = 1 / sqrt(sum u^2 + eps) of a q or k head:
+//   du = r (dq - u r^2 <u, dq>)  (v: du = dv),   dy = du act'(y),
+//   dx[s] = sum_i w_i dy[s + 3 - i],   dw_i = sum_t dy[t] x[t - 3 + i].
+//
+// HBM-bound: raw rows and output gradients read once, raw gradients written once.
+// One warp walks a run of consecutive tokens of one head, each lane holding 4 channels:
+// a rolling window of three raw rows feeds the convolution, three partial rows of dx
+// wait for the tokens ahead of them, and dw runs in registers.  Runs overlap by the
+// three rows behind and ahead of them.
+struct FrontendGradParams {
+    FrontendGradArgs a;
+    float* part;  // [runs, (2 H_qk + H_v) d, 4] partial sums of dw
+    int runs, run_len, blocks;  // blocks of the convolution part; the rest take the gates
+};
+
+__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
+    return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z),
+                       fmaf(a.w, b.w, c.w));
+}
+__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
+    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
+__device__ __forceinline__ float dot4(float4 a, float4 b) {
+    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+}
+
+constexpr int FG_WARPS = 4;
+
+template <typename IO, int ACT>
+__global__ void __launch_bounds__(FG_WARPS * 32) frontend_grad_kernel(const FrontendGradParams p) {
+    const FrontendGradArgs& a = p.a;
+    const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
+    if ((int)blockIdx.x >= p.blocks) {  // the gates, element by element
+        const int64_t n = (int64_t)T_end * a.H_v;
+        const int64_t step = (int64_t)(gridDim.x - p.blocks) * (FG_WARPS * 32);
+        for (int64_t i = (int64_t)(blockIdx.x - p.blocks) * (FG_WARPS * 32) + threadIdx.x; i < n;
+             i += step) {
+            const float be = sigmoidf(a.b[i]);
+            a.da[i] = -sigmoidf(a.a[i]) * a.dlog_alpha[i];
+            a.db[i] = be * (1.f - be) * a.dbeta[i];
+        }
+        return;
+    }
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int heads = 2 * a.H_qk + a.H_v;
+    const int64_t unit = (int64_t)blockIdx.x * FG_WARPS + warp;
+    if (unit >= (int64_t)p.runs * heads) return;
+    const int run = (int)(unit / heads), hid = (int)(unit - (int64_t)run * heads);
+    const int kind = hid < a.H_qk ? 0 : (hid < 2 * a.H_qk ? 1 : 2);
+    const int head = hid - (kind == 0 ? 0 : (kind == 1 ? a.H_qk : 2 * a.H_qk));
+    const int64_t rs = (int64_t)(kind == 2 ? a.H_v : a.H_qk) * FD;
+    const int64_t off = (int64_t)head * FD + 4 * lane;
+    const IO* x = static_cast<const IO*>(kind == 0 ? a.x[0] : (kind == 1 ? a.x[1] : a.x[2])) + off;
+    const IO* go =
+        static_cast<const IO*>(kind == 0 ? a.dout[0] : (kind == 1 ? a.dout[1] : a.dout[2])) + off;
+    IO* dx = static_cast<IO*>(kind == 0 ? a.dx[0] : (kind == 1 ? a.dx[1] : a.dx[2])) + off;
+
+    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+    float4 w[4], dw[4] = {z, z, z, z};
+    {
+        const float4* wp = reinterpret_cast<const float4*>(a.w + ((int64_t)hid * FD + 4 * lane) * 4);
+        const float4 c0 = wp[0], c1 = wp[1], c2 = wp[2], c3 = wp[3];
+        w[0] = make_float4(c0.x, c1.x, c2.x, c3.x);
+        w[1] = make_float4(c0.y, c1.y, c2.y, c3.y);
+        w[2] = make_float4(c0.z, c1.z, c2.z, c3.z);
+        w[3] = make_float4(c0.w, c1.w, c2.w, c3.w);
+    }
+
+    const int64_t first = (int64_t)run * p.run_len;
+    const int ta = (int)min(first, (int64_t)T_end), tb = (int)min(first + p.run_len, (int64_t)T_end);
+    if (ta < tb) {
+        // the sequence of token ta, and where the next one starts
+        int n = 0, s = 0, next = T_end;
+        if (a.cu_seqlens) {
+            int hi = a.N - 1;
+            while (n < hi) {
+                const int mid = (n + hi + 1) >> 1;
+                if (a.cu_seqlens[mid] <= ta) n = mid; else hi = mid - 1;
+            }
+            s = max(a.cu_seqlens[n], 0);
+            next = a.cu_seqlens[n + 1];
+        }
+        float4 x1 = ta - 1 >= s ? Vec4<IO>::load(x + (ta - 1) * rs) : z;
+        float4 x2 = ta - 2 >= s ? Vec4<IO>::load(x + (ta - 2) * rs) : z;
+        float4 x3 = ta - 3 >= s ? Vec4<IO>::load(x + (ta - 3) * rs) : z;
+        float4 d1 = z, d2 = z, d3 = z;  // dx of tokens t - 1, t - 2, t - 3 so far
+        int lo = max(s, ta);            // the first token whose dx is pending or stored here
+        const int te = min(tb + 3, T_end);
+        int t = ta;
+        for (; t < te; ++t) {
+            if (t == next) {  // a sequence starts: what waits has no tokens ahead of it
+                if (t - 3 >= lo && t - 3 < tb) Vec4<IO>::store(dx + (t - 3) * rs, d3);
+                if (t - 2 >= lo && t - 2 < tb) Vec4<IO>::store(dx + (t - 2) * rs, d2);
+                if (t - 1 >= lo && t - 1 < tb) Vec4<IO>::store(dx + (t - 1) * rs, d1);
+                x1 = x2 = x3 = d1 = d2 = d3 = z;
+                lo = t;
+                do {
+                    ++n;
+                } while (n + 1 < a.N && a.cu_seqlens[n + 1] <= t);
+                next = a.cu_seqlens[n + 1];
+                if (t >= tb) break;
+            }
+            const float4 x0 = Vec4<IO>::load(x + t * rs);
+            float4 dy = Vec4<IO>::load(go + t * rs);
+            float4 y = conv4(w, x3, x2, x1, x0), u = y, slope = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (ACT == GDN_ACT_SILU) {
+                const float4 sg =
+                    make_float4(sigmoidf(y.x), sigmoidf(y.y), sigmoidf(y.z), sigmoidf(y.w));
+                u = mul4(y, sg);
+                slope = make_float4(fmaf(u.x, 1.f - sg.x, sg.x), fmaf(u.y, 1.f - sg.y, sg.y),
+                                    fmaf(u.z, 1.f - sg.z, sg.z), fmaf(u.w, 1.f - sg.w, sg.w));
+            }
+            if (kind < 2) {
+                float ss = dot4(u, u), ud = dot4(u, dy);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) {
+                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
+                    ud += __shfl_xor_sync(0xffffffffu, ud, o);
+                }
+                const float r = rsqrtf(ss + a.eps), c = -r * r * r * ud;
+                dy = make_float4(fmaf(u.x, c, r * dy.x), fmaf(u.y, c, r * dy.y),
+                                 fmaf(u.z, c, r * dy.z), fmaf(u.w, c, r * dy.w));
+            }
+            if (ACT == GDN_ACT_SILU) dy = mul4(dy, slope);
+            if (t < tb) {
+                dw[0] = fma4(dy, x3, dw[0]);
+                dw[1] = fma4(dy, x2, dw[1]);
+                dw[2] = fma4(dy, x1, dw[2]);
+                dw[3] = fma4(dy, x0, dw[3]);
+            }
+            d3 = fma4(w[0], dy, d3);
+            if (t - 3 >= lo) Vec4<IO>::store(dx + (t - 3) * rs, d3);
+            d3 = fma4(w[1], dy, d2);
+            d2 = fma4(w[2], dy, d1);
+            d1 = mul4(w[3], dy);
+            x3 = x2;
+            x2 = x1;
+            x1 = x0;
+        }
+        if (t == te) {  // the end of the run (or of the tokens)
+            if (t - 3 >= lo && t - 3 < tb) Vec4<IO>::store(dx + (t - 3) * rs, d3);
+            if (t - 2 >= lo && t - 2 < tb) Vec4<IO>::store(dx + (t - 2) * rs, d2);
+            if (t - 1 >= lo && t - 1 < tb) Vec4<IO>::store(dx + (t - 1) * rs, d1);
+        }
+    }
+    float4* o = reinterpret_cast<float4*>(p.part) + ((int64_t)run * heads + hid) * FD + 4 * lane;
+    o[0] = make_float4(dw[0].x, dw[1].x, dw[2].x, dw[3].x);
+    o[1] = make_float4(dw[0].y, dw[1].y, dw[2].y, dw[3].y);
+    o[2] = make_float4(dw[0].z, dw[1].z, dw[2].z, dw[3].z);
+    o[3] = make_float4(dw[0].w, dw[1].w, dw[2].w, dw[3].w);
+}
+
+// Runs per head: enough warps for the SMs, runs of at least 32 tokens.
+int frontend_grad_runs(int T, int heads) {
+    const long long want = ((long long)device_sms() * 24 + heads - 1) / heads;
+    const long long most = ((long long)T + 31) / 32;
+    const long long r = want < most ? want : most;
+    return (int)(r < 1 ? 1 : r);
+}
+
 }  // namespace
+
+size_t frontend_backward_workspace_bytes(int T, int H_qk, int H_v) {
+    const int heads = 2 * H_qk + H_v;
+    return T == 0 ? 0 : (size_t)frontend_grad_runs(T, heads) * heads * FD * 4 * sizeof(float);
+}
+
+cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
+                                     cudaStream_t stream) {
+    const int heads = 2 * a.H_qk + a.H_v;
+    FrontendGradParams p{};
+    p.a = a;
+    p.part = static_cast<float*>(workspace);
+    if (a.T > 0) {
+        p.runs = frontend_grad_runs(a.T, heads);
+        p.run_len = (a.T + p.runs - 1) / p.runs;
+        const long long blocks = ((long long)p.runs * heads + FG_WARPS - 1) / FG_WARPS;
+        const long long gates = ((long long)a.T * a.H_v + 1023) / 1024;  // 8 or more per thread
+        const long long gate_blocks = gates < 148 ? gates : 148;
+        if (blocks + gate_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+        p.blocks = (int)blocks;
+        const unsigned grid = (unsigned)(blocks + gate_blocks);
+        if (a.bf16) {
+            if (a.silu)
+                frontend_grad_kernel<__nv_bfloat16, GDN_ACT_SILU><<<grid, FG_WARPS * 32, 0, stream>>>(p);
+            else
+                frontend_grad_kernel<__nv_bfloat16, GDN_ACT_NONE><<<grid, FG_WARPS * 32, 0, stream>>>(p);
+        } else {
+            if (a.silu)
+                frontend_grad_kernel<float, GDN_ACT_SILU><<<grid, FG_WARPS * 32, 0, stream>>>(p);
+            else
+                frontend_grad_kernel<float, GDN_ACT_NONE><<<grid, FG_WARPS * 32, 0, stream>>>(p);
+        }
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return launch_column_sums(p.part, nullptr, a.dw, nullptr, p.runs, heads * FD * 4, stream);
+}
 
 cudaError_t launch_frontend(const void* q_raw, const void* k_raw, const void* v_raw,
                             const float* conv_w, const float* a, const float* b,

@@ -119,6 +119,26 @@ size_t group_norm_backward_workspace_bytes(int T, int H, int d, int weight_heads
 cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, float* dbias,
                                        void* workspace, cudaStream_t stream);
 
+// out0 = column sums of part0 [rows, cols] in a fixed order, and out1 of part1 unless null.
+cudaError_t launch_column_sums(const float* part0, const float* part1, float* out0, float* out1,
+                               int rows, int cols, cudaStream_t stream);
+
+// Gradients of the front end.
+struct FrontendGradArgs {
+    const void* x[3];     // q_raw, k_raw, v_raw
+    const void* dout[3];  // dq, dk, dv
+    void* dx[3];
+    const float *w, *a, *b, *dlog_alpha, *dbeta;
+    float *dw, *da, *db;
+    const int32_t* cu_seqlens;
+    int N, T, H_qk, H_v;
+    bool bf16, silu;
+    float eps;
+};
+size_t frontend_backward_workspace_bytes(int T, int H_qk, int H_v);
+cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
+                                     cudaStream_t stream);
+
 cudaError_t read_and_clear_status(unsigned int* status, cudaStream_t stream);
 
 // Fixed-size device scratch used by gdn_prefill_noalloc (bytes, and its address

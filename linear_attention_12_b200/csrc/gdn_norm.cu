@@ -305,8 +305,8 @@ __global__ void __launch_bounds__(NT) group_norm_backward_kernel(const NormParam
     }
 }
 
-// Column sums of part [rows, cols] into out (blockIdx.y: dweight, then dbias), in
-// an order that does not depend on the grid.
+// Column sums of part [rows, cols] into out (blockIdx.y: the first pair, then the
+// second), in an order that does not depend on timing.
 __global__ void __launch_bounds__(256)
     column_sums_kernel(const float* part0, const float* part1, float* out0, float* out1, int rows,
                        int cols) {
@@ -437,6 +437,13 @@ int partial_rows(int T, int H, int d, bool per_head, int ve) {
 
 }  // namespace
 
+cudaError_t launch_column_sums(const float* part0, const float* part1, float* out0, float* out1,
+                               int rows, int cols, cudaStream_t stream) {
+    column_sums_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 256, 0, stream>>>(
+        part0, part1, out0, out1, rows, cols);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream) {
     if (a.T == 0) return cudaSuccess;
     return launch_any(params_of(a), a.bf16, FWD_BLOCKS, false, stream);
@@ -471,9 +478,7 @@ cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, f
         if (e != cudaSuccess) return e;
         rows = partial_rows(a.T, a.H, a.d, per_head, vector_of(p, a.bf16));
     }
-    column_sums_kernel<<<dim3((cols + 31) / 32, dbias ? 2 : 1), 256, 0, stream>>>(
-        p.dw_part, p.db_part, dweight, dbias, rows, cols);
-    return cudaGetLastError();
+    return launch_column_sums(p.dw_part, p.db_part, dweight, dbias, rows, cols, stream);
 }
 
 }  // namespace gdn

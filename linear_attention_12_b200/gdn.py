@@ -93,6 +93,10 @@ SIGNATURES = {
                                 [_c.c_void_p, _c.c_int64] * 2 + [_c.c_void_p] * 3 +
                                 [_c.c_size_t, _c.c_void_p]),
     "gdn_group_norm_backward_workspace_size": (_c.c_size_t, [_c.c_int32] * 4 + [_c.c_int]),
+    "gdn_frontend_backward": (_c.c_int, [_c.c_void_p] * 12 + [_c.c_int32] * 6 +
+                              [_c.c_int, _c.c_int, _c.c_float] + [_c.c_void_p] * 7 +
+                              [_c.c_size_t, _c.c_void_p]),
+    "gdn_frontend_backward_workspace_size": (_c.c_size_t, [_c.c_int32] * 5 + [_c.c_int]),
     "gdn_get_last_device_error": (_c.c_int, [_c.c_void_p]),
     "gdn_selftest_bounded_wait": (_c.c_int, [_c.c_void_p]),
     "gdn_status_string": (_c.c_char_p, [_c.c_int]),
@@ -715,6 +719,48 @@ def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="si
     if st != GDN_OK:
         raise GDNError(st, "gdn_group_norm_backward")
     return dx, dw, db, dz
+
+
+@_placed
+def frontend_backward(q_raw, k_raw, v_raw, conv_w, a, b, dq, dk, dv, dlog_alpha, dbeta,
+                      cu_seqlens=None, *, act="none", eps=1e-6, workspace=None):
+    """Gradients of :func:`frontend` (gdn_frontend_backward): from those of q, k, v, log_alpha
+    and beta (``prefill_backward``'s results) to those of its inputs.
+
+    Returns ``(dq_raw, dk_raw, dv_raw, dconv_w, da, db)``: the first three in the inputs'
+    type, the others fp32.  Rows from ``cu_seqlens[-1]`` on stay unwritten."""
+    if q_raw.dim() != 3 or v_raw.dim() != 3:
+        raise ValueError("q_raw, k_raw and v_raw must be [T, H, d]")
+    io, dt, dev = _dtype_of(q_raw, "q_raw"), q_raw.dtype, q_raw.device
+    T, H_qk, dk_ = q_raw.shape
+    H_v, dv_ = v_raw.shape[1:]
+    for t, name in ((q_raw, "q_raw"), (k_raw, "k_raw"), (dq, "dq"), (dk, "dk")):
+        _dense(t, name, dt, q_raw.shape, dev)
+    for t, name in ((v_raw, "v_raw"), (dv, "dv")):
+        _dense(t, name, dt, (T, H_v, dv_), dev)
+    for t, name in ((a, "a"), (b, "b"), (dlog_alpha, "dlog_alpha"), (dbeta, "dbeta")):
+        _dense(t, name, torch.float32, (T, H_v), dev)
+    _dense(conv_w, "conv_w", torch.float32, ((2 * H_qk + H_v) * dk_, 4), dev)
+    _, _, _, N, cu = _scan_sizes(q_raw, cu_seqlens, dev)
+    dq_raw, dk_raw, dv_raw = (torch.empty(t.shape, dtype=dt, device=dev)
+                              for t in (q_raw, k_raw, v_raw))
+    dw = torch.empty(conv_w.shape, dtype=torch.float32, device=dev)
+    da, db = (torch.empty((T, H_v), dtype=torch.float32, device=dev) for _ in range(2))
+    L = lib()
+    if workspace is None:
+        workspace = _workspace(None, L.gdn_frontend_backward_workspace_size(T, H_qk, H_v, dk_, dv_,
+                                                                            io), dev)
+    else:
+        _workspace(workspace, 0, dev)
+    st = L.gdn_frontend_backward(
+        q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), conv_w.data_ptr(), a.data_ptr(),
+        b.data_ptr(), cu, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlog_alpha.data_ptr(),
+        dbeta.data_ptr(), N, T, H_qk, H_v, dk_, dv_, io, _choice(act, _ACTS, "act"), eps,
+        dq_raw.data_ptr(), dk_raw.data_ptr(), dv_raw.data_ptr(), dw.data_ptr(), da.data_ptr(),
+        db.data_ptr(), _at(workspace), _nbytes(workspace), _here(dev))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_frontend_backward")
+    return dq_raw, dk_raw, dv_raw, dw, da, db
 
 
 def selftest_bounded_wait(stream=None) -> None:
