@@ -460,7 +460,9 @@ gdn_status check_frontend_sizes(int32_t T, int32_t H_qk, int32_t H_v, int32_t dk
 
 gdn_status check_scan(const int32_t* cu_seqlens, int32_t N, int32_t T, int32_t C, gdn_dtype io,
                       gdn_dtype gate) {
-    if (N <= 0 || T < 0 || C <= 0 || T > (1 << 30) || C > (1 << 22)) return GDN_ERR_INVALID_ARG;
+    if (N <= 0 || T < 0 || C <= 0 || T > (1 << 30) || N > (1 << 30) ||
+        C > (1 << 22))
+        return GDN_ERR_INVALID_ARG;
     if ((io != GDN_BF16 && io != GDN_F32) || (gate != GDN_BF16 && gate != GDN_F32))
         return GDN_ERR_INVALID_ARG;
     if ((long long)T * C >= (1ll << 40) || (long long)N * C >= (1ll << 40))
