@@ -10,6 +10,8 @@
 // All of it is HBM-bound: 3 flops and one exp per element.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
@@ -37,7 +39,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 // joined in order, and every piece then runs again from the state that enters it.  Here
 // the data is read once and stays in registers between the two runs:
 //
-//   * A block takes a tile of TT = 8 ST tokens x 64 channels; warp g holds ST consecutive
+//   * A block takes a tile of TT = WARPS ST tokens x 64 channels; warp g holds ST consecutive
 //     tokens, each lane two channels.
 //   * A cluster of R blocks takes R consecutive tiles of the same 64 channels at a time and
 //     walks over all tokens.  Each block sends its tile's (A, B) into the shared memory of
@@ -45,7 +47,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 //     so each knows the state entering its own tile and the next R tiles.
 //
 // No block waits for anything outside its cluster, nothing goes through global memory, and
-// the order of every sum is fixed by the sizes alone.  A ninth warp keeps STAGES tiles on
+// the order of every sum is fixed by the sizes alone.  One more warp keeps STAGES tiles on
 // their way by TMA and works out which rows start or end a sequence.
 //
 // Packed sequences are one token axis: a row that starts a sequence (for the gradients,
@@ -53,9 +55,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 // a row carry A = -1 and drop the state by selection, not by a product with 0, so that an
 // infinity or a NaN cannot cross.
 constexpr int CW = 64;             // channels of a tile
-constexpr int WARPS = 8;           // consumer warps: time groups of a tile
-constexpr int THREADS = (WARPS + 1) * 32;
 constexpr int MAX_CLUSTER = 8;
+constexpr int MAX_DEVICES = 16;    // whose cluster room is remembered
 constexpr int SCAN_BAR = 1;        // named barrier of the consumer warps
 
 struct ScanParams {
@@ -68,24 +69,120 @@ struct ScanParams {
     int N, T, C;
 };
 
-// Two neighbouring channels.
-__device__ __forceinline__ float2 two(const float* p) { return *reinterpret_cast<const float2*>(p); }
-__device__ __forceinline__ float2 two(const __nv_bfloat16* p) {
-    const uint32_t u = *reinterpret_cast<const uint32_t*>(p);
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-}
+// Two neighbouring channels, as stored (bf16 pairs stay packed in one register) and widened.
+template <typename T>
+struct Pair;
+template <>
+struct Pair<float> {
+    using Raw = float2;
+    static __device__ __forceinline__ Raw make(float a, float b) { return make_float2(a, b); }
+    static __device__ __forceinline__ float2 widen(Raw v) { return v; }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    using Raw = uint32_t;
+    static __device__ __forceinline__ Raw make(float a, float b) { return pack_bf16x2(a, b); }
+    static __device__ __forceinline__ float2 widen(Raw u) {
+        return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    }
+};
+// A tile in shared memory and its two channels of a lane.  TILED: rows of CW channels as the
+// tensor copy wrote them, neighbours 2 lane and 2 lane + 1.  Else: rows of 16-byte granules
+// whose first holds the row's first channel somewhere inside (`shift` bytes in, another one
+// for every row), channels lane and lane + 32, which keeps the scalar accesses coalesced.
+template <typename T, bool TILED>
+struct Tile {
+    static constexpr int PITCH = CW * (int)sizeof(T) + (TILED ? 0 : 16);
+    static __device__ __forceinline__ uint32_t shift(const void* base, int64_t row, int64_t stride,
+                                                     int c0) {
+        const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(base);
+        return (at + ((uint32_t)row * (uint32_t)stride + (uint32_t)c0) * (uint32_t)sizeof(T)) & 15u;
+    }
+    static __device__ __forceinline__ typename Pair<T>::Raw at(const uint8_t* tile, int r, int lane,
+                                                               const void* base, int64_t row,
+                                                               int64_t stride, int c0) {
+        if (TILED)
+            return reinterpret_cast<const typename Pair<T>::Raw*>(tile + r * PITCH)[lane];
+        const T* p = reinterpret_cast<const T*>(tile + r * PITCH + shift(base, row, stride, c0));
+        return Pair<T>::make(to_f(p[lane]), to_f(p[lane + 32]));
+    }
+    // The granules of one row that hold its n channels from c0 on.
+    static __device__ __forceinline__ const uint8_t* granule(const void* base, int64_t row,
+                                                             int64_t stride, int c0) {
+        return reinterpret_cast<const uint8_t*>(
+            reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * stride + c0) &
+            ~(uintptr_t)15);
+    }
+    static __device__ __forceinline__ uint32_t bytes(const void* base, int64_t row, int64_t stride,
+                                                     int c0, int n) {
+        return (shift(base, row, stride, c0) + n * (uint32_t)sizeof(T) + 15u) & ~15u;
+    }
+};
 __device__ __forceinline__ void put_two(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
 __device__ __forceinline__ void put_two(__nv_bfloat16* p, float2 v) {
     *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.x, v.y);
 }
 
-// The map (A, B) of two channels, the later one q after p, and a map applied to a state.
-__device__ __forceinline__ void compose1(float& pa, float& pb, float qa, float qb) {
-    pb = qa < 0.f ? qb : fmaf(qa, pb, qb);
-    pa = qa < 0.f || pa < 0.f ? -1.f : pa * qa;
+// Two channels in one instruction (the FP32 pipe's paired form).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+        "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
 }
-__device__ __forceinline__ float apply1(float qa, float qb, float s) {
-    return qa < 0.f ? qb : fmaf(qa, s, qb);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "mul.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+        "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+        "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// exp by the base-2 instruction: its own error is 2 ulp, and the product with log2(e) adds
+// |v| 2^-24, which is small where the gate is not.  (expf's range checks cost 6 more
+// instructions per element, and instructions are what this kernel runs out of first.)
+__device__ __forceinline__ float2 exp2ch(float2 v) {
+    const float2 w = mul2(v, make_float2(1.4426950408889634f, 1.4426950408889634f));
+    float2 r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(w.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(w.y));
+    return r;
+}
+
+// A map s -> A s + B of two channels.
+struct Map {
+    float2 a, b;
+};
+__device__ __forceinline__ float4 as4(const Map& m) {
+    return make_float4(m.a.x, m.a.y, m.b.x, m.b.y);
+}
+__device__ __forceinline__ Map as_map(float4 v) {
+    return Map{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+// q after p, and q applied to a state; A < 0: the state that comes in is dropped.
+__device__ __forceinline__ Map compose(const Map& p, const Map& q) {
+    if (q.a.x < 0.f) return q;  // (both channels reset together)
+    Map r;
+    r.b = fma2(q.a, p.b, q.b);
+    r.a = p.a.x < 0.f ? p.a : mul2(p.a, q.a);
+    return r;
+}
+__device__ __forceinline__ float2 apply(const Map& q, float2 s) {
+    return q.a.x < 0.f ? q.b : fma2(q.a, s, q.b);
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -138,11 +235,11 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 }
 
 // Shared memory of a block.
-template <typename IO, typename G, bool BWD, bool TMA, int ST, int STAGES>
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES>
 struct ScanSmem {
     static constexpr int TT = WARPS * ST;
-    static constexpr int X = TMA ? TT * CW * (int)sizeof(IO) : 0;
-    static constexpr int L = TMA ? TT * CW * (int)sizeof(G) : 0;
+    static constexpr int X = TT * Tile<IO, TMA>::PITCH;
+    static constexpr int L = TT * Tile<G, TMA>::PITCH;
     static constexpr int DATA = X + L + (BWD ? X : 0);  // x (dh), log_alpha, h
     struct Meta {
         uint32_t reset[WARPS], emit[WARPS];  // one bit per row of a time group, scan order
@@ -153,14 +250,14 @@ struct ScanSmem {
     static constexpr int SLOT = AGG + 2 * WARPS * 32 * 16;
     static constexpr int BARS = SLOT + 2 * MAX_CLUSTER * 32 * 16;
     static constexpr int BYTES = BARS + (2 * STAGES + 2) * 8 + 16;
-    static_assert(sizeof(Meta) % 16 == 0 && DATA % 128 == 0, "regions stay aligned");
+    static_assert(sizeof(Meta) % 16 == 0 && X % 128 == 0 && L % 128 == 0, "regions stay aligned");
 };
 
-template <typename IO, typename G, bool BWD, bool TMA, int ST, int STAGES, int MINB>
-__global__ void __launch_bounds__(THREADS, MINB)
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES, int MINB>
+__global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_la,
                 const __grid_constant__ CUtensorMap map_h, const ScanParams p, const int R) {
-    using SM = ScanSmem<IO, G, BWD, TMA, ST, STAGES>;
+    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST, STAGES>;
     using Meta = typename SM::Meta;
     constexpr int TT = SM::TT;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -197,15 +294,38 @@ __global__ void __launch_bounds__(THREADS, MINB)
             const int st = it % STAGES, k = it * R + rank;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
             if (it >= STAGES) mbar_wait(&empty[st], (it / STAGES - 1) & 1, abort_flag);
-            if (lane == 0) {
-                if (TMA) {
-                    uint8_t* d = sm + st * SM::DATA;
+            uint8_t* d = sm + st * SM::DATA;
+            if (TMA) {
+                if (lane == 0) {
                     mbar_arrive_expect_tx(&full[st], SM::DATA);
                     tma_load_2d(d, &map_x, c0, row0, &full[st]);
                     tma_load_2d(d + SM::X, &map_la, c0, row0, &full[st]);
                     if (BWD) tma_load_2d(d + SM::X + SM::L, &map_h, c0, row0 - 1, &full[st]);
-                } else {
-                    mbar_arrive(&full[st]);
+                }
+            } else {
+                // row by row, the 16-byte granules that hold it (rows that are not used stay out)
+                const int rows = min(TT, T_end - row0), n = min(CW, p.C - c0);
+                uint32_t total = 0;
+                for (int r = lane; r < rows; r += 32) {
+                    total += Tile<IO, TMA>::bytes(p.x, row0 + r, p.xs, c0, n) +
+                             Tile<G, TMA>::bytes(p.la, row0 + r, p.las, c0, n);
+                    if (BWD && row0 + r > 0)
+                        total += Tile<IO, TMA>::bytes(p.h, row0 + r - 1, p.hs, c0, n);
+                }
+                total = __reduce_add_sync(0xffffffffu, total);
+                if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
+                __syncwarp();
+                const auto copy = [&](auto t, uint8_t* to, const void* base, int64_t row, int64_t s) {
+                    using E = Tile<decltype(t), TMA>;
+                    bulk_load(to, E::granule(base, row, s, c0), E::bytes(base, row, s, c0, n),
+                              &full[st]);
+                };
+                for (int r = lane; r < rows; r += 32) {
+                    copy(IO(), d + r * Tile<IO, TMA>::PITCH, p.x, row0 + r, p.xs);
+                    copy(G(), d + SM::X + r * Tile<G, TMA>::PITCH, p.la, row0 + r, p.las);
+                    if (BWD && row0 + r > 0)
+                        copy(IO(), d + SM::X + SM::L + r * Tile<IO, TMA>::PITCH, p.h, row0 + r - 1,
+                             p.hs);
                 }
             }
             Meta& m = metas[st];
@@ -252,8 +372,9 @@ __global__ void __launch_bounds__(THREADS, MINB)
         __syncwarp();
     } else {
         // ---- consumers ----
-        const int c = c0 + 2 * lane;
-        const bool has0 = c < p.C, has1 = c + 1 < p.C;
+        constexpr int NEXT = TMA ? 1 : 32;  // a lane's second channel
+        const int c = c0 + (TMA ? 2 * lane : lane);
+        const bool has0 = c < p.C, has1 = c + NEXT < p.C;
         // sequences without tokens hand their state through
         if (p.last && (p.cu || T_end == 0)) {
             for (int n0 = (rank * WARPS + warp) * 32; n0 < p.N; n0 += R * WARPS * 32) {
@@ -264,156 +385,140 @@ __global__ void __launch_bounds__(THREADS, MINB)
                     const int64_t o = (int64_t)(n0 + __ffs(none) - 1) * p.C + c;
                     none &= none - 1;
                     if (has0) p.last[o] = p.init ? p.init[o] : 0.f;
-                    if (has1) p.last[o + 1] = p.init ? p.init[o + 1] : 0.f;
+                    if (has1) p.last[o + NEXT] = p.init ? p.init[o + NEXT] : 0.f;
                 }
             }
         }
-        float s0 = 0.f, s1 = 0.f;  // the state entering the R tiles of this iteration
+        float2 state = make_float2(0.f, 0.f);  // entering the R tiles of this iteration
         for (int it = 0; it < iters; ++it) {
             const int st = it % STAGES, k = it * R + rank, b = it & 1;
             const bool live = k < ntiles;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
-            float2 a[ST], x[ST], before[BWD ? ST : 1];
+            const Meta& m = metas[st];
+            float2 a[ST], kept = make_float2(0.f, 0.f);
+            typename Pair<IO>::Raw x[ST], before[BWD ? ST : 1];
             uint32_t reset = 0u, emit = 0u;
-            float A0 = 1.f, A1 = 1.f, B0 = 0.f, B1 = 0.f;
+            Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+            // what a reset row starts from: the state given for its sequence
+            const auto given = [&](int j) {
+                if (!p.init) return make_float2(0.f, 0.f);
+                const float* i = p.init + (int64_t)m.reset_n[warp * ST + j] * p.C + c;
+                return make_float2(has0 ? i[0] : 0.f, has1 ? i[NEXT] : 0.f);
+            };
+            // h (or u) of a row, from the row's before it in scan order
+            const auto step = [&](int j, float2 s) {
+                const float2 xj = Pair<IO>::widen(x[j]);
+                return BWD ? mul2(a[j], add2(s, xj)) : fma2(a[j], s, xj);
+            };
             if (live) {
-                const Meta& m = metas[st];
                 if (mbar_wait(&full[st], (it / STAGES) & 1, abort_flag)) {
                     reset = m.reset[warp];
                     emit = m.emit[warp];
                 }
                 const uint8_t* d = sm + st * SM::DATA;
+                typename Pair<G>::Raw l[ST];
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
                     const int r = BWD ? TT - 1 - (warp * ST + j) : warp * ST + j;
-                    float2 l;
-                    if (TMA) {
-                        x[j] = two(reinterpret_cast<const IO*>(d) + r * CW + 2 * lane);
-                        l = two(reinterpret_cast<const G*>(d + SM::X) + r * CW + 2 * lane);
-                        if (BWD)
-                            before[j] =
-                                two(reinterpret_cast<const IO*>(d + SM::X + SM::L) + r * CW + 2 * lane);
-                    } else {
-                        const int64_t t = row0 + r;
-                        const bool in = t < T_end;
-                        const IO* px = static_cast<const IO*>(p.x) + t * p.xs + c;
-                        const G* pl = static_cast<const G*>(p.la) + t * p.las + c;
-                        x[j] = make_float2(in && has0 ? to_f(px[0]) : 0.f, in && has1 ? to_f(px[1]) : 0.f);
-                        l = make_float2(in && has0 ? to_f(pl[0]) : 0.f, in && has1 ? to_f(pl[1]) : 0.f);
-                        if (BWD) {
-                            const bool inb = in && t > 0;
-                            const IO* ph = static_cast<const IO*>(p.h) + (t - 1) * p.hs + c;
-                            before[j] = make_float2(inb && has0 ? to_f(ph[0]) : 0.f,
-                                                    inb && has1 ? to_f(ph[1]) : 0.f);
-                        }
-                    }
-                    a[j] = make_float2(expf(l.x), expf(l.y));
+                    const int64_t t = row0 + r;
+                    l[j] = Tile<G, TMA>::at(d + SM::X, r, lane, p.la, t, p.las, c0);
+                    x[j] = Tile<IO, TMA>::at(d, r, lane, p.x, t, p.xs, c0);
+                    if (BWD)
+                        before[j] =
+                            Tile<IO, TMA>::at(d + SM::X + SM::L, r, lane, p.h, t - 1, p.hs, c0);
                 }
-                if (reset | emit) {
-                    // rows that add the state of their sequence
+#pragma unroll
+                for (int j = 0; j < ST; ++j) a[j] = exp2ch(Pair<G>::widen(l[j]));
+                // the map of these ST rows
+                if (reset) {
 #pragma unroll
                     for (int j = 0; j < ST; ++j) {
-                        if (reset >> j & 1 && p.init) {
-                            const int64_t o = (int64_t)m.reset_n[warp * ST + j] * p.C + c;
-                            const float i0 = has0 ? p.init[o] : 0.f, i1 = has1 ? p.init[o + 1] : 0.f;
-                            // (the gradients multiply by the gate behind the sum)
-                            x[j].x = BWD ? x[j].x + i0 : fmaf(a[j].x, i0, x[j].x);
-                            x[j].y = BWD ? x[j].y + i1 : fmaf(a[j].y, i1, x[j].y);
-                        }
-                        if (BWD && emit >> j & 1) {
-                            const int64_t o = (int64_t)m.emit_n[warp * ST + j] * p.C + c;
-                            before[j].x = p.h0 && has0 ? p.h0[o] : 0.f;
-                            before[j].y = p.h0 && has1 ? p.h0[o + 1] : 0.f;
-                        }
+                        if (reset >> j & 1) mine.b = kept = given(j);
+                        mine.b = step(j, mine.b);
+                    }
+                    mine.a = make_float2(-1.f, -1.f);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < ST; ++j) {
+                        mine.b = step(j, mine.b);
+                        mine.a = mul2(mine.a, a[j]);
                     }
                 }
-                if (!emit) {  // nothing of the stage is read again
+                if (!(reset | emit)) {  // nothing of the stage is read again
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&empty[st]);
                 }
-                // the map of these ST rows
-#pragma unroll
-                for (int j = 0; j < ST; ++j) {
-                    if (reset >> j & 1) B0 = B1 = 0.f;
-                    if (BWD) {
-                        B0 = a[j].x * (B0 + x[j].x);
-                        B1 = a[j].y * (B1 + x[j].y);
-                    } else {
-                        B0 = fmaf(a[j].x, B0, x[j].x);
-                        B1 = fmaf(a[j].y, B1, x[j].y);
-                    }
-                    A0 *= a[j].x;
-                    A1 *= a[j].y;
-                }
-                if (reset) A0 = A1 = -1.f;
             }
-            agg[(b * WARPS + warp) * 32 + lane] = make_float4(A0, B0, A1, B1);
+            agg[(b * WARPS + warp) * 32 + lane] = as4(mine);
             bar_sync<SCAN_BAR, WARPS * 32>();
             // the map of the time groups before this one, within the tile
-            float pa0 = 1.f, pa1 = 1.f, pb0 = 0.f, pb1 = 0.f;
-            for (int q = 0; q < warp; ++q) {
-                const float4 v = agg[(b * WARPS + q) * 32 + lane];
-                compose1(pa0, pb0, v.x, v.y);
-                compose1(pa1, pb1, v.z, v.w);
-            }
+            Map pre{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
+            for (int q = 0; q < warp; ++q)
+                pre = compose(pre, as_map(agg[(b * WARPS + q) * 32 + lane]));
             if (warp == WARPS - 1) {  // the whole tile's map goes to every block
                 if (lane == 0) mbar_arrive_expect_tx(&joined[b], R * 32 * 16);
-                float4 v = make_float4(pa0, pb0, pa1, pb1);
-                compose1(v.x, v.y, A0, B0);
-                compose1(v.z, v.w, A1, B1);
+                const float4 v = as4(compose(pre, mine));
                 const uint32_t to = smem_u32(&slot[(b * MAX_CLUSTER + rank) * 32 + lane]);
                 const uint32_t bar = smem_u32(&joined[b]);
                 for (int r = 0; r < R; ++r) st_async(map_rank(to, r), v, map_rank(bar, r));
             }
             mbar_wait_cluster(&joined[b], (it >> 1) & 1, abort_flag);
-            float h0 = s0, h1 = s1;
+            float2 h = state;
             for (int r = 0; r < R; ++r) {
-                if (r == rank) h0 = s0, h1 = s1;
-                const float4 v = slot[(b * MAX_CLUSTER + r) * 32 + lane];
-                s0 = apply1(v.x, v.y, s0);
-                s1 = apply1(v.z, v.w, s1);
+                if (r == rank) h = state;
+                state = apply(as_map(slot[(b * MAX_CLUSTER + r) * 32 + lane]), state);
             }
             if (!live) continue;
-            h0 = apply1(pa0, pb0, h0);
-            h1 = apply1(pa1, pb1, h1);
+            h = apply(pre, h);
             // the rows once more, from the state that enters them
-            const Meta& m = metas[st];
+            const int r0 = BWD ? TT - 1 - warp * ST : warp * ST;
+            constexpr int DIR = BWD ? -1 : 1;
+            IO* po = static_cast<IO*>(p.out) + (int64_t)(row0 + r0) * p.outs + c;
+            G* pg = BWD ? static_cast<G*>(p.dla) + (int64_t)(row0 + r0) * p.dlas + c : nullptr;
+            if (TMA && !(reset | emit) && row0 + TT <= T_end && c0 + CW <= p.C) {
 #pragma unroll
-            for (int j = 0; j < ST; ++j) {
-                const int r = BWD ? TT - 1 - (warp * ST + j) : warp * ST + j;
-                const int64_t t = row0 + r;
-                if (reset >> j & 1) h0 = h1 = 0.f;
-                float2 o, g;
-                if (BWD) {
-                    o = make_float2(x[j].x + h0, x[j].y + h1);
-                    h0 = a[j].x * o.x;
-                    h1 = a[j].y * o.y;
-                    g = make_float2(h0 * before[j].x, h1 * before[j].y);
-                } else {
-                    h0 = fmaf(a[j].x, h0, x[j].x);
-                    h1 = fmaf(a[j].y, h1, x[j].y);
-                    o = make_float2(h0, h1);
-                }
-                if (t < T_end) {
-                    IO* po = static_cast<IO*>(p.out) + t * p.outs + c;
-                    G* pg = BWD ? static_cast<G*>(p.dla) + t * p.dlas + c : nullptr;
-                    if (TMA && has1) {
-                        put_two(po, o);
-                        if (BWD) put_two(pg, g);
-                    } else {
-                        if (has0) po[0] = from_f<IO>(o.x);
-                        if (has1) po[1] = from_f<IO>(o.y);
-                        if (BWD && has0) pg[0] = from_f<G>(g.x);
-                        if (BWD && has1) pg[1] = from_f<G>(g.y);
+                for (int j = 0; j < ST; ++j) {
+                    const float2 o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
+                    h = BWD ? mul2(a[j], o) : o;
+                    put_two(po, o);
+                    po += DIR * p.outs;
+                    if (BWD) {
+                        put_two(pg, mul2(h, Pair<IO>::widen(before[j])));
+                        pg += DIR * p.dlas;
                     }
                 }
-                if (emit >> j & 1 && p.last) {
-                    const int64_t at = (int64_t)m.emit_n[warp * ST + j] * p.C + c;
-                    if (has0) p.last[at] = h0;
-                    if (has1) p.last[at + 1] = h1;
+            } else {
+#pragma unroll
+                for (int j = 0; j < ST; ++j) {
+                    // (the last reset row's state may be overwritten by now, where the sequence
+                    // ends in another warp and the result goes in its place: it was kept)
+                    if (reset >> j & 1) h = reset >> j == 1u ? kept : given(j);
+                    const float2 o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
+                    h = BWD ? mul2(a[j], o) : o;
+                    const bool out = emit >> j & 1;
+                    const int64_t at = out ? (int64_t)m.emit_n[warp * ST + j] * p.C + c : 0;
+                    if (row0 + r0 + DIR * j < T_end) {
+                        if (has0) po[0] = from_f<IO>(o.x);
+                        if (has1) po[NEXT] = from_f<IO>(o.y);
+                        if (BWD) {
+                            float2 w = Pair<IO>::widen(before[j]);
+                            if (out)  // the first token of its sequence
+                                w = make_float2(p.h0 && has0 ? p.h0[at] : 0.f,
+                                                p.h0 && has1 ? p.h0[at + NEXT] : 0.f);
+                            const float2 g = mul2(h, w);
+                            if (has0) pg[0] = from_f<G>(g.x);
+                            if (has1) pg[NEXT] = from_f<G>(g.y);
+                        }
+                    }
+                    po += DIR * p.outs;
+                    if (BWD) pg += DIR * p.dlas;
+                    if (out && p.last) {
+                        if (has0) p.last[at] = h.x;
+                        if (has1) p.last[at + NEXT] = h.y;
+                    }
                 }
             }
-            if (emit) {
+            if (reset | emit) {
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);
             }
@@ -464,10 +569,10 @@ bool wide_rows(const void* ptr, int64_t stride, int elem) {
     return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride * elem % 16 == 0;
 }
 
-template <typename IO, typename G, bool BWD, bool TMA, int ST, int STAGES, int MINB>
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES, int MINB>
 cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
-    using SM = ScanSmem<IO, G, BWD, TMA, ST, STAGES>;
-    const auto kernel = scan_kernel<IO, G, BWD, TMA, ST, STAGES, MINB>;
+    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST, STAGES>;
+    const auto kernel = scan_kernel<IO, G, BWD, TMA, WARPS, ST, STAGES, MINB>;
     CUtensorMap mx{}, ml{}, mh{};
     if (TMA && p.T > 0) {
         if (!tile_map(&mx, p.x, sizeof(IO) == 2, p.T, p.C, p.xs, SM::TT) ||
@@ -478,23 +583,38 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
     if (e != cudaSuccess) return e;
-    // blocks per cluster: as many as the SMs hold at once, and no more than there are tiles
-    const long long groups = ((long long)p.C + CW - 1) / CW;
-    const long long tiles = ((long long)p.T + SM::TT - 1) / SM::TT;
-    const long long room = (long long)device_sms() * MINB;
-    int R = 1;
-    while (R < MAX_CLUSTER && R < tiles && groups * (2 * R) <= room) R *= 2;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(groups * R));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3((WARPS + 1) * 32);
     cfg.dynamicSmemBytes = SM::BYTES;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = R;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[0].val.clusterDim.x = attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    // Blocks per cluster: the most with which all clusters run at once (a second wave costs as
+    // much as the first), and no more than there are tiles.
+    const long long groups = ((long long)p.C + CW - 1) / CW;
+    const long long tiles = ((long long)p.T + SM::TT - 1) / SM::TT;
+    static std::atomic<int> room[MAX_DEVICES][MAX_CLUSTER + 1];  // 0: not asked yet
+    int dev = 0;
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
+    int R = (int)(tiles < MAX_CLUSTER ? (tiles < 1 ? 1 : tiles) : MAX_CLUSTER);
+    for (; R > 1; --R) {
+        int fit = dev < MAX_DEVICES ? room[dev][R].load(std::memory_order_relaxed) : 0;
+        if (fit == 0) {
+            cfg.gridDim = dim3(R);
+            attr[0].val.clusterDim.x = R;
+            if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess || fit < 1) {
+                cudaGetLastError();
+                fit = -1;
+            }
+            if (dev < MAX_DEVICES) room[dev][R].store(fit, std::memory_order_relaxed);
+        }
+        if (groups <= fit) break;
+    }
+    attr[0].val.clusterDim.x = R;
+    cfg.gridDim = dim3((unsigned)(groups * R));
     return cudaLaunchKernelEx(&cfg, kernel, mx, ml, mh, p, R);
 }
 
@@ -505,9 +625,9 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
                       wide_rows(p.out, p.outs, e) &&
                       (!BWD || (wide_rows(p.h, p.hs, e) && wide_rows(p.dla, p.dlas, ge)));
     constexpr int STAGES = 2;
-    constexpr int MINB = BWD ? 2 : 3;
-    if (wide) return launch_tiles<IO, G, BWD, true, 8, STAGES, MINB>(p, stream);
-    return launch_tiles<IO, G, BWD, false, 8, STAGES, MINB>(p, stream);
+    constexpr int WARPS = 4, ST = 16, MINB = 3;
+    if (wide) return launch_tiles<IO, G, BWD, true, WARPS, ST, STAGES, MINB>(p, stream);
+    return launch_tiles<IO, G, BWD, false, WARPS, ST, STAGES, MINB>(p, stream);
 }
 
 template <bool BWD>
