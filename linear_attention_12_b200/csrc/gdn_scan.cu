@@ -185,6 +185,17 @@ __device__ __forceinline__ float2 apply(const Map& q, float2 s) {
     return q.a.x < 0.f ? q.b : fma2(q.a, s, q.b);
 }
 
+// Asynchronous 16-byte copies of a thread, in groups.
+__device__ __forceinline__ void cp_async16(void* to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -245,8 +256,9 @@ struct ScanSmem {
         uint32_t reset[WARPS], emit[WARPS];  // one bit per row of a time group, scan order
         int reset_n[TT], emit_n[TT];         // their sequences
     };
+    static constexpr int METAS = STAGES + 1;  // read until the tile is written, one tile longer
     static constexpr int META = STAGES * DATA;
-    static constexpr int AGG = META + STAGES * (int)sizeof(Meta);
+    static constexpr int AGG = META + METAS * (int)sizeof(Meta);
     static constexpr int SLOT = AGG + 2 * WARPS * 32 * 16;
     static constexpr int BARS = SLOT + 2 * MAX_CLUSTER * 32 * 16;
     static constexpr int BYTES = BARS + (2 * STAGES + 2) * 8 + 16;
@@ -277,7 +289,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) {
-            mbar_init(&full[i], 2);
+            mbar_init(&full[i], TMA ? 2 : 1);  // the copies, and the rows' marks
             mbar_init(&empty[i], WARPS);
         }
         mbar_init(&joined[0], 1);
@@ -294,41 +306,14 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             const int st = it % STAGES, k = it * R + rank;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
             if (it >= STAGES) mbar_wait(&empty[st], (it / STAGES - 1) & 1, abort_flag);
-            uint8_t* d = sm + st * SM::DATA;
-            if (TMA) {
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&full[st], SM::DATA);
-                    tma_load_2d(d, &map_x, c0, row0, &full[st]);
-                    tma_load_2d(d + SM::X, &map_la, c0, row0, &full[st]);
-                    if (BWD) tma_load_2d(d + SM::X + SM::L, &map_h, c0, row0 - 1, &full[st]);
-                }
-            } else {
-                // row by row, the 16-byte granules that hold it (rows that are not used stay out)
-                const int rows = min(TT, T_end - row0), n = min(CW, p.C - c0);
-                uint32_t total = 0;
-                for (int r = lane; r < rows; r += 32) {
-                    total += Tile<IO, TMA>::bytes(p.x, row0 + r, p.xs, c0, n) +
-                             Tile<G, TMA>::bytes(p.la, row0 + r, p.las, c0, n);
-                    if (BWD && row0 + r > 0)
-                        total += Tile<IO, TMA>::bytes(p.h, row0 + r - 1, p.hs, c0, n);
-                }
-                total = __reduce_add_sync(0xffffffffu, total);
-                if (lane == 0) mbar_arrive_expect_tx(&full[st], total);
-                __syncwarp();
-                const auto copy = [&](auto t, uint8_t* to, const void* base, int64_t row, int64_t s) {
-                    using E = Tile<decltype(t), TMA>;
-                    bulk_load(to, E::granule(base, row, s, c0), E::bytes(base, row, s, c0, n),
-                              &full[st]);
-                };
-                for (int r = lane; r < rows; r += 32) {
-                    copy(IO(), d + r * Tile<IO, TMA>::PITCH, p.x, row0 + r, p.xs);
-                    copy(G(), d + SM::X + r * Tile<G, TMA>::PITCH, p.la, row0 + r, p.las);
-                    if (BWD && row0 + r > 0)
-                        copy(IO(), d + SM::X + SM::L + r * Tile<IO, TMA>::PITCH, p.h, row0 + r - 1,
-                             p.hs);
-                }
+            if (TMA && lane == 0) {
+                uint8_t* d = sm + st * SM::DATA;
+                mbar_arrive_expect_tx(&full[st], SM::DATA);
+                tma_load_2d(d, &map_x, c0, row0, &full[st]);
+                tma_load_2d(d + SM::X, &map_la, c0, row0, &full[st]);
+                if (BWD) tma_load_2d(d + SM::X + SM::L, &map_h, c0, row0 - 1, &full[st]);
             }
-            Meta& m = metas[st];
+            Meta& m = metas[it % SM::METAS];
             if (lane < WARPS) m.reset[lane] = m.emit[lane] = 0u;
             __syncwarp();
             int n = 0;  // the last sequence that starts at or before row0
@@ -389,22 +374,55 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
             }
         }
+        // Unaligned rows: every warp copies its own, the 16-byte granules that hold them, STAGES
+        // turns ahead (rows that are not used stay out).
+        const auto fetch = [&](int it) {
+            const int k = it * R + rank;
+            if (k < ntiles) {
+                const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
+                const int r0 = BWD ? TT - (warp + 1) * ST : warp * ST;  // the group's lowest row
+                const int n = min(CW, p.C - c0);
+                uint8_t* d = sm + it % STAGES * SM::DATA;
+                const auto copy = [&](auto t, uint8_t* tile, const void* base, int back, int64_t s) {
+                    using E = Tile<decltype(t), TMA>;
+                    constexpr int GR = E::PITCH / 16;
+                    for (int q = lane; q < ST * GR; q += 32) {
+                        const int r = r0 + q / GR, o = q % GR * 16, row = row0 + r - back;
+                        if (row >= 0 && row0 + r < T_end && o < (int)E::bytes(base, row, s, c0, n))
+                            cp_async16(tile + r * E::PITCH + o, E::granule(base, row, s, c0) + o);
+                    }
+                };
+                copy(G(), d + SM::X, p.la, 0, p.las);
+                copy(IO(), d, p.x, 0, p.xs);
+                if (BWD) copy(IO(), d + SM::X + SM::L, p.h, 1, p.hs);
+            }
+            cp_async_commit();
+        };
+        if (!TMA)
+            for (int it = 0; it < STAGES; ++it) fetch(it);
+
         float2 state = make_float2(0.f, 0.f);  // entering the R tiles of this iteration
         for (int it = 0; it < iters; ++it) {
             const int st = it % STAGES, k = it * R + rank, b = it & 1;
             const bool live = k < ntiles;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
-            const Meta& m = metas[st];
-            float2 a[ST], kept = make_float2(0.f, 0.f);
+            const Meta& m = metas[it % SM::METAS];
+            float2 a[ST];
             typename Pair<IO>::Raw x[ST], before[BWD ? ST : 1];
             uint32_t reset = 0u, emit = 0u;
             Map mine{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
-            // what a reset row starts from: the state given for its sequence
-            const auto given = [&](int j) {
-                if (!p.init) return make_float2(0.f, 0.f);
-                const float* i = p.init + (int64_t)m.reset_n[warp * ST + j] * p.C + c;
-                return make_float2(has0 ? i[0] : 0.f, has1 ? i[NEXT] : 0.f);
+            // channels of a row of states
+            const auto states = [&](const float* base, int n) {
+                if (!base) return make_float2(0.f, 0.f);
+                base += (int64_t)n * p.C + c;
+                return make_float2(has0 ? base[0] : 0.f, has1 ? base[NEXT] : 0.f);
             };
+            // The state given to the group's last sequence and h0 of its first: almost always the
+            // only ones, and asked for early.  (The first matters for more: where that sequence
+            // ends in another warp, its result may take the given state's place before this warp
+            // runs again.)
+            int last_reset = -1, first_emit = -1;
+            float2 kept = make_float2(0.f, 0.f), kept_h0 = kept;
             // h (or u) of a row, from the row's before it in scan order
             const auto step = [&](int j, float2 s) {
                 const float2 xj = Pair<IO>::widen(x[j]);
@@ -415,7 +433,19 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                     reset = m.reset[warp];
                     emit = m.emit[warp];
                 }
+                if (reset) {
+                    last_reset = 31 - __clz(reset);
+                    kept = states(p.init, m.reset_n[warp * ST + last_reset]);
+                }
+                if (BWD && emit) {
+                    first_emit = __ffs(emit) - 1;
+                    kept_h0 = states(p.h0, m.emit_n[warp * ST + first_emit]);
+                }
                 const uint8_t* d = sm + st * SM::DATA;
+                if (!TMA) {
+                    cp_async_wait<STAGES - 1>();
+                    __syncwarp();
+                }
                 typename Pair<G>::Raw l[ST];
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
@@ -429,13 +459,14 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
 #pragma unroll
                 for (int j = 0; j < ST; ++j) a[j] = exp2ch(Pair<G>::widen(l[j]));
-                // the map of these ST rows
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);  // the tile is in registers
+                if (!TMA) fetch(it + STAGES);
+                // the map of these ST rows (only what follows the last reset counts)
                 if (reset) {
 #pragma unroll
-                    for (int j = 0; j < ST; ++j) {
-                        if (reset >> j & 1) mine.b = kept = given(j);
-                        mine.b = step(j, mine.b);
-                    }
+                    for (int j = 0; j < ST; ++j)
+                        mine.b = step(j, j == last_reset ? kept : mine.b);
                     mine.a = make_float2(-1.f, -1.f);
                 } else {
 #pragma unroll
@@ -443,10 +474,6 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                         mine.b = step(j, mine.b);
                         mine.a = mul2(mine.a, a[j]);
                     }
-                }
-                if (!(reset | emit)) {  // nothing of the stage is read again
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&empty[st]);
                 }
             }
             agg[(b * WARPS + warp) * 32 + lane] = as4(mine);
@@ -464,6 +491,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             }
             mbar_wait_cluster(&joined[b], (it >> 1) & 1, abort_flag);
             float2 h = state;
+#pragma unroll 4
             for (int r = 0; r < R; ++r) {
                 if (r == rank) h = state;
                 state = apply(as_map(slot[(b * MAX_CLUSTER + r) * 32 + lane]), state);
@@ -475,54 +503,71 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             constexpr int DIR = BWD ? -1 : 1;
             IO* po = static_cast<IO*>(p.out) + (int64_t)(row0 + r0) * p.outs + c;
             G* pg = BWD ? static_cast<G*>(p.dla) + (int64_t)(row0 + r0) * p.dlas + c : nullptr;
+            // o: the row's output, g: its second one (the gradients' dlog_alpha)
+            const auto run = [&](int j, float2& o, float2& g, float2 w) {
+                o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
+                h = BWD ? mul2(a[j], o) : o;
+                if (BWD) g = mul2(h, w);
+            };
+            const auto put = [&](int j, float2 o, float2 g) {
+                if (row0 + r0 + DIR * j < T_end) {
+                    if (has0) po[0] = from_f<IO>(o.x);
+                    if (has1) po[NEXT] = from_f<IO>(o.y);
+                    if (BWD && has0) pg[0] = from_f<G>(g.x);
+                    if (BWD && has1) pg[NEXT] = from_f<G>(g.y);
+                }
+                po += DIR * p.outs;
+                if (BWD) pg += DIR * p.dlas;
+            };
+            const auto finish = [&](int j, float2 s) {  // the state behind a sequence
+                if (!p.last) return;
+                float* to = p.last + (int64_t)m.emit_n[warp * ST + j] * p.C + c;
+                if (has0) to[0] = s.x;
+                if (has1) to[NEXT] = s.y;
+            };
+            // Three forms of the same loop: rows without marks, groups with one boundary (no branch
+            // inside: the rows' instructions interleave, which halves the time), and the rest.
             if (TMA && !(reset | emit) && row0 + TT <= T_end && c0 + CW <= p.C) {
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
-                    const float2 o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
-                    h = BWD ? mul2(a[j], o) : o;
+                    float2 o, g;
+                    run(j, o, g, Pair<IO>::widen(before[BWD ? j : 0]));
                     put_two(po, o);
                     po += DIR * p.outs;
                     if (BWD) {
-                        put_two(pg, mul2(h, Pair<IO>::widen(before[j])));
+                        put_two(pg, g);
                         pg += DIR * p.dlas;
                     }
                 }
+            } else if (!(reset & (reset - 1)) && !(emit & (emit - 1))) {
+                const int emit_at = emit ? __ffs(emit) - 1 : -1;
+                float2 ended = h;
+#pragma unroll
+                for (int j = 0; j < ST; ++j) {
+                    float2 o, g;
+                    if (j == last_reset) h = kept;
+                    run(j, o, g,
+                        BWD && j == emit_at ? kept_h0 : Pair<IO>::widen(before[BWD ? j : 0]));
+                    if (j == emit_at) ended = h;
+                    put(j, o, g);
+                }
+                if (emit) finish(emit_at, ended);
             } else {
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
-                    // (the last reset row's state may be overwritten by now, where the sequence
-                    // ends in another warp and the result goes in its place: it was kept)
-                    if (reset >> j & 1) h = reset >> j == 1u ? kept : given(j);
-                    const float2 o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
-                    h = BWD ? mul2(a[j], o) : o;
-                    const bool out = emit >> j & 1;
-                    const int64_t at = out ? (int64_t)m.emit_n[warp * ST + j] * p.C + c : 0;
-                    if (row0 + r0 + DIR * j < T_end) {
-                        if (has0) po[0] = from_f<IO>(o.x);
-                        if (has1) po[NEXT] = from_f<IO>(o.y);
-                        if (BWD) {
-                            float2 w = Pair<IO>::widen(before[j]);
-                            if (out)  // the first token of its sequence
-                                w = make_float2(p.h0 && has0 ? p.h0[at] : 0.f,
-                                                p.h0 && has1 ? p.h0[at + NEXT] : 0.f);
-                            const float2 g = mul2(h, w);
-                            if (has0) pg[0] = from_f<G>(g.x);
-                            if (has1) pg[NEXT] = from_f<G>(g.y);
-                        }
-                    }
-                    po += DIR * p.outs;
-                    if (BWD) pg += DIR * p.dlas;
-                    if (out && p.last) {
-                        if (has0) p.last[at] = h.x;
-                        if (has1) p.last[at + NEXT] = h.y;
-                    }
+                    float2 o, g;
+                    if (reset >> j & 1)
+                        h = j == last_reset ? kept : states(p.init, m.reset_n[warp * ST + j]);
+                    float2 w = Pair<IO>::widen(before[BWD ? j : 0]);
+                    if (BWD && emit >> j & 1)
+                        w = j == first_emit ? kept_h0 : states(p.h0, m.emit_n[warp * ST + j]);
+                    run(j, o, g, w);
+                    if (emit >> j & 1) finish(j, h);
+                    put(j, o, g);
                 }
             }
-            if (reset | emit) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
-            }
         }
+        cp_async_wait<0>();
     }
     cluster_sync();  // nobody ends while others may still send to it
 }
@@ -624,10 +669,16 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
     const bool wide = wide_rows(p.x, p.xs, e) && wide_rows(p.la, p.las, ge) &&
                       wide_rows(p.out, p.outs, e) &&
                       (!BWD || (wide_rows(p.h, p.hs, e) && wide_rows(p.dla, p.dlas, ge)));
-    constexpr int STAGES = 2;
-    constexpr int WARPS = 4, ST = 16, MINB = 3;
-    if (wide) return launch_tiles<IO, G, BWD, true, WARPS, ST, STAGES, MINB>(p, stream);
-    return launch_tiles<IO, G, BWD, false, WARPS, ST, STAGES, MINB>(p, stream);
+    // Few channels leave one block an SM or less: larger tiles then, for fewer turns of the cluster.
+    const bool few = ((long long)p.C + CW - 1) / CW * MAX_CLUSTER <= device_sms();
+    if (few) {
+        // (16 rows a warp do not fit the shared memory where three unaligned fp32 tiles are held)
+        constexpr int ST = BWD && sizeof(IO) + sizeof(G) == 8 ? 8 : 16;
+        return wide ? launch_tiles<IO, G, BWD, true, 8, 16, 2, 1>(p, stream)
+                    : launch_tiles<IO, G, BWD, false, 8, ST, 2, 1>(p, stream);
+    }
+    return wide ? launch_tiles<IO, G, BWD, true, 4, 16, 2, 3>(p, stream)
+                : launch_tiles<IO, G, BWD, false, 4, 16, 2, 3>(p, stream);
 }
 
 template <bool BWD>
