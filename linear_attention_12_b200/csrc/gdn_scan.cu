@@ -47,7 +47,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 //     so each knows the state entering its own tile and the next R tiles.
 //
 // No block waits for anything outside its cluster, nothing goes through global memory, and
-// the order of every sum is fixed by the sizes alone.  One more warp keeps STAGES tiles on
+// the order of every sum is fixed by the sizes alone.  One more warp keeps one or two tiles on
 // their way by TMA and works out which rows start or end a sequence.
 //
 // Packed sequences are one token axis: a row that starts a sequence (for the gradients,
@@ -246,7 +246,7 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
 }
 
 // Shared memory of a block.
-template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES>
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST>
 struct ScanSmem {
     static constexpr int TT = WARPS * ST;
     static constexpr int X = TT * Tile<IO, TMA>::PITCH;
@@ -256,20 +256,21 @@ struct ScanSmem {
         uint32_t reset[WARPS], emit[WARPS];  // one bit per row of a time group, scan order
         int reset_n[TT], emit_n[TT];         // their sequences
     };
-    static constexpr int METAS = STAGES + 1;  // read until the tile is written, one tile longer
-    static constexpr int META = STAGES * DATA;
+    static constexpr int METAS = 3;  // read until the tile is written, one tile longer
+    static constexpr int META = 2 * DATA;
     static constexpr int AGG = META + METAS * (int)sizeof(Meta);
     static constexpr int SLOT = AGG + 2 * WARPS * 32 * 16;
     static constexpr int BARS = SLOT + 2 * MAX_CLUSTER * 32 * 16;
-    static constexpr int BYTES = BARS + (2 * STAGES + 2) * 8 + 16;
+    static constexpr int BYTES = BARS + 6 * 8 + 16;
     static_assert(sizeof(Meta) % 16 == 0 && X % 128 == 0 && L % 128 == 0, "regions stay aligned");
 };
 
-template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES, int MINB>
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int MINB>
 __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     scan_kernel(const __grid_constant__ CUtensorMap map_x, const __grid_constant__ CUtensorMap map_la,
-                const __grid_constant__ CUtensorMap map_h, const ScanParams p, const int R) {
-    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST, STAGES>;
+                const __grid_constant__ CUtensorMap map_h, const ScanParams p, const int R,
+                const int two_stages) {
+    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST>;
     using Meta = typename SM::Meta;
     constexpr int TT = SM::TT;
     extern __shared__ __align__(128) uint8_t sm[];
@@ -277,8 +278,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     float4* agg = reinterpret_cast<float4*>(sm + SM::AGG);    // [2][WARPS][32]
     float4* slot = reinterpret_cast<float4*>(sm + SM::SLOT);  // [2][MAX_CLUSTER][32]
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + SM::BARS);
-    uint64_t* empty = full + STAGES;
-    uint64_t* joined = empty + STAGES;  // [2]
+    uint64_t* empty = full + 2;
+    uint64_t* joined = empty + 2;
     volatile int* abort_flag = reinterpret_cast<volatile int*>(joined + 2);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -288,12 +289,11 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     const int ntiles = (T_end + TT - 1) / TT, iters = (ntiles + R - 1) / R;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], TMA ? 2 : 1);  // the copies, and the rows' marks
             mbar_init(&empty[i], WARPS);
+            mbar_init(&joined[i], 1);
         }
-        mbar_init(&joined[0], 1);
-        mbar_init(&joined[1], 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -303,9 +303,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
         // ---- producer: tiles by TMA, and the rows where sequences start and end ----
         int it = 0;
         for (; it * R + rank < ntiles; ++it) {
-            const int st = it % STAGES, k = it * R + rank;
+            const int st = it & two_stages, turn = it >> two_stages, k = it * R + rank;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
-            if (it >= STAGES) mbar_wait(&empty[st], (it / STAGES - 1) & 1, abort_flag);
+            if (turn > 0) mbar_wait(&empty[st], (turn - 1) & 1, abort_flag);
             if (TMA && lane == 0) {
                 uint8_t* d = sm + st * SM::DATA;
                 mbar_arrive_expect_tx(&full[st], SM::DATA);
@@ -349,8 +349,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
         if (*abort_flag && lane == 0) {
             // copies may still be landing: let them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
-            for (int j = max(0, it - STAGES); j < it; ++j)
-                while (!mbar_try_wait(smem_u32(&full[j % STAGES]), (j / STAGES) & 1) &&
+            for (int j = max(0, it - 1 - two_stages); j < it; ++j)
+                while (!mbar_try_wait(smem_u32(&full[j & two_stages]), (j >> two_stages) & 1) &&
                        globaltimer() - ts < kWaitLimitNs) {
                 }
         }
@@ -374,7 +374,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
             }
         }
-        // Unaligned rows: every warp copies its own, the 16-byte granules that hold them, STAGES
+        // Unaligned rows: every warp copies its own, the 16-byte granules that hold them, two
         // turns ahead (rows that are not used stay out).
         const auto fetch = [&](int it) {
             const int k = it * R + rank;
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
                 const int r0 = BWD ? TT - (warp + 1) * ST : warp * ST;  // the group's lowest row
                 const int n = min(CW, p.C - c0);
-                uint8_t* d = sm + it % STAGES * SM::DATA;
+                uint8_t* d = sm + (it & 1) * SM::DATA;
                 const auto copy = [&](auto t, uint8_t* tile, const void* base, int back, int64_t s) {
                     using E = Tile<decltype(t), TMA>;
                     constexpr int GR = E::PITCH / 16;
@@ -399,11 +399,11 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             cp_async_commit();
         };
         if (!TMA)
-            for (int it = 0; it < STAGES; ++it) fetch(it);
+            for (int it = 0; it < 2; ++it) fetch(it);
 
         float2 state = make_float2(0.f, 0.f);  // entering the R tiles of this iteration
         for (int it = 0; it < iters; ++it) {
-            const int st = it % STAGES, k = it * R + rank, b = it & 1;
+            const int st = it & two_stages, k = it * R + rank, b = it & 1;
             const bool live = k < ntiles;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
             const Meta& m = metas[it % SM::METAS];
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 return BWD ? mul2(a[j], add2(s, xj)) : fma2(a[j], s, xj);
             };
             if (live) {
-                if (mbar_wait(&full[st], (it / STAGES) & 1, abort_flag)) {
+                if (mbar_wait(&full[st], (it >> two_stages) & 1, abort_flag)) {
                     reset = m.reset[warp];
                     emit = m.emit[warp];
                 }
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
                 const uint8_t* d = sm + st * SM::DATA;
                 if (!TMA) {
-                    cp_async_wait<STAGES - 1>();
+                    cp_async_wait<1>();
                     __syncwarp();
                 }
                 typename Pair<G>::Raw l[ST];
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 for (int j = 0; j < ST; ++j) a[j] = exp2ch(Pair<G>::widen(l[j]));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);  // the tile is in registers
-                if (!TMA) fetch(it + STAGES);
+                if (!TMA) fetch(it + 2);
                 // the map of these ST rows (only what follows the last reset counts)
                 if (reset) {
 #pragma unroll
@@ -614,10 +614,10 @@ bool wide_rows(const void* ptr, int64_t stride, int elem) {
     return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride * elem % 16 == 0;
 }
 
-template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int STAGES, int MINB>
+template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST, int MINB>
 cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
-    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST, STAGES>;
-    const auto kernel = scan_kernel<IO, G, BWD, TMA, WARPS, ST, STAGES, MINB>;
+    using SM = ScanSmem<IO, G, BWD, TMA, WARPS, ST>;
+    const auto kernel = scan_kernel<IO, G, BWD, TMA, WARPS, ST, MINB>;
     CUtensorMap mx{}, ml{}, mh{};
     if (TMA && p.T > 0) {
         if (!tile_map(&mx, p.x, sizeof(IO) == 2, p.T, p.C, p.xs, SM::TT) ||
@@ -660,7 +660,13 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     }
     attr[0].val.clusterDim.x = R;
     cfg.gridDim = dim3((unsigned)(groups * R));
-    return cudaLaunchKernelEx(&cfg, kernel, mx, ml, mh, p, R);
+    // A second tile on its way hides the first one's latency.  The gradients' five streams
+    // stand more in flight badly: past what the memory system needs it only lengthens the
+    // queues, clusters progress unevenly and the last ones run alone.  32,768 x 6144 bf16
+    // gradients took 410 us with 18.9 MB in flight and 331 us with 9.4 MB; the forward with
+    // fp32 gates took 246 us with 18.9 MB and 270 us with 9.4 MB.
+    const int two = !BWD || !TMA || groups * R * (2ll * SM::DATA) <= (15 << 20);
+    return cudaLaunchKernelEx(&cfg, kernel, mx, ml, mh, p, R, two);
 }
 
 template <typename IO, typename G, bool BWD>
@@ -674,11 +680,11 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
     if (few) {
         // (16 rows a warp do not fit the shared memory where three unaligned fp32 tiles are held)
         constexpr int ST = BWD && sizeof(IO) + sizeof(G) == 8 ? 8 : 16;
-        return wide ? launch_tiles<IO, G, BWD, true, 8, 16, 2, 1>(p, stream)
-                    : launch_tiles<IO, G, BWD, false, 8, ST, 2, 1>(p, stream);
+        return wide ? launch_tiles<IO, G, BWD, true, 8, 16, 1>(p, stream)
+                    : launch_tiles<IO, G, BWD, false, 8, ST, 1>(p, stream);
     }
-    return wide ? launch_tiles<IO, G, BWD, true, 4, 16, 2, 3>(p, stream)
-                : launch_tiles<IO, G, BWD, false, 4, 16, 2, 3>(p, stream);
+    return wide ? launch_tiles<IO, G, BWD, true, 4, 16, 3>(p, stream)
+                : launch_tiles<IO, G, BWD, false, 4, 16, 3>(p, stream);
 }
 
 template <bool BWD>
