@@ -11,7 +11,10 @@
 // Both directions are HBM-bound: one pass over the data, a group's channels in
 // the registers of LG lanes, its statistics by shuffles.  A lane group keeps one
 // head and walks over the tokens, so that the weights stay in registers and the
-// sums of dw and db run in registers over all its tokens.
+// sums of dw and db run in registers over all its tokens; the next token's
+// channels are on their way while one is computed.  The arithmetic goes two
+// channels to an instruction: at one each, the gradients' ~35 instructions per
+// channel take as long as their 10 bytes.
 #include <cuda_bf16.h>
 
 #include "../../include/gdn.h"
@@ -22,54 +25,17 @@ namespace gdn {
 
 namespace {
 
-constexpr int NT = 256;       // threads per block
-constexpr int FWD_BLOCKS = 8;  // blocks per SM the grids are sized for
-constexpr int BWD_BLOCKS = 4;
-
-// VE consecutive channels as floats.
-template <typename IO, int VE>
-struct Chan;
-template <>
-struct Chan<__nv_bfloat16, 8> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[8]) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[8]) {
-        *reinterpret_cast<uint4*>(p) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                       pack_bf16x2(v[6], v[7]));
-    }
-};
-template <>
-struct Chan<float, 4> {
-    static __device__ __forceinline__ void load(const float* p, float (&v)[4]) {
-        const float4 u = *reinterpret_cast<const float4*>(p);
-        v[0] = u.x, v[1] = u.y, v[2] = u.z, v[3] = u.w;
-    }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[4]) {
-        *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-};
-template <>
-struct Chan<__nv_bfloat16, 1> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16* p, float (&v)[1]) {
-        v[0] = __bfloat162float(*p);
-    }
-    static __device__ __forceinline__ void store(__nv_bfloat16* p, const float (&v)[1]) {
-        *p = __float2bfloat16_rn(v[0]);
-    }
-};
-template <>
-struct Chan<float, 1> {
-    static __device__ __forceinline__ void load(const float* p, float (&v)[1]) { v[0] = *p; }
-    static __device__ __forceinline__ void store(float* p, const float (&v)[1]) { *p = v[0]; }
-};
+constexpr int NT = 256;        // threads per block
+// Blocks per SM that the grids are sized for, so that all run at once: as many as the
+// registers allow without spills in the loop.  (The gradients with bias or mean and bf16's
+// eight channels a lane need 128: at three blocks 516 us, at two 379 us, for 32,768 x 48 x 128.
+// The others took 332 us at three and 371 us at two.  Forward, with a gate: 201 us at four
+// and 295 us at five; without gate, mean and bias: 152 us and 143 us.)
+constexpr int fwd_blocks(bool gated, bool plain) { return !gated && plain ? 5 : 4; }
+constexpr int bwd_blocks(bool plain, bool bf16_wide) { return !plain && bf16_wide ? 2 : 3; }
+// Tokens that a lane group of the gradients walks over at least: its partial sums (fp32, one
+// row per stream for weights per head) cost as much traffic as two to four tokens.
+constexpr int BWD_TOKENS = 4;
 
 struct NormParams {
     const void *x, *z, *dy;
@@ -77,12 +43,92 @@ struct NormParams {
     const float *w, *b;
     float *dw_part, *db_part;
     int64_t xs, zs, dys, ys, dzs;  // row strides in elements
-    int T, H, d, nvec, streams;
+    int T, H, d, streams;
     bool per_head, centred, silu, has_bias;
     float eps, inv_d;
 };
 
-__device__ __forceinline__ float sigmoid_fast(float y) { return __fdividef(1.f, 1.f + __expf(-y)); }
+// The channels of a group that a lane holds, in NV vectors of NP pairs.  WIDE: 16 bytes
+// each, channels (lane + LG j) VE .. + VE - 1 of vector j.  Else one pair each, channels
+// lane + 2 LG j and LG further, so that scalar accesses stay coalesced.
+template <typename IO, bool WIDE, int LG>
+struct Vec {
+    static constexpr int VE = WIDE ? 16 / (int)sizeof(IO) : 2;
+    static constexpr int NP = VE / 2;
+    static constexpr int STEP = WIDE ? 1 : LG;  // from a pair's first channel to its second
+    struct Raw {
+        uint32_t u[WIDE ? 4 : 2];
+    };
+    static __device__ __forceinline__ int channel(int lane, int j, int i) {
+        return WIDE ? (lane + LG * j) * VE + 2 * i : lane + 2 * LG * j;
+    }
+    // p: the group's first channel
+    static __device__ __forceinline__ Raw load(const IO* p, int lane, int j, int d, bool ok) {
+        Raw r;
+        const int c = channel(lane, j, 0);
+        if constexpr (WIDE) {
+            uint4 u = make_uint4(0u, 0u, 0u, 0u);
+            if (ok && c < d) u = *reinterpret_cast<const uint4*>(p + c);
+            r.u[0] = u.x, r.u[1] = u.y, r.u[2] = u.z, r.u[3] = u.w;
+        } else {
+            const float a = ok && c < d ? (float)p[c] : 0.f;
+            const float b = ok && c + STEP < d ? (float)p[c + STEP] : 0.f;
+            r.u[0] = __float_as_uint(a), r.u[1] = __float_as_uint(b);
+        }
+        return r;
+    }
+    static __device__ __forceinline__ float2 pair(const Raw& r, int i) {
+        if constexpr (WIDE && sizeof(IO) == 2)
+            return make_float2(__uint_as_float(r.u[i] << 16), __uint_as_float(r.u[i] & 0xffff0000u));
+        else
+            return make_float2(__uint_as_float(r.u[2 * i]), __uint_as_float(r.u[2 * i + 1]));
+    }
+    static __device__ __forceinline__ void store(IO* p, int lane, int j, int d, bool ok,
+                                                 const float2 (&v)[NP]) {
+        const int c = channel(lane, j, 0);
+        if constexpr (WIDE && sizeof(IO) == 2) {
+            if (ok && c < d)
+                *reinterpret_cast<uint4*>(p + c) =
+                    make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
+        } else if constexpr (WIDE) {
+            if (ok && c < d)
+                *reinterpret_cast<float4*>(p + c) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+        } else {
+            if (ok && c < d) p[c] = (IO)v[0].x;
+            if (ok && c + STEP < d) p[c + STEP] = (IO)v[0].y;
+        }
+    }
+    static __device__ __forceinline__ float2 weight(const float* w, int lane, int j, int i, int d) {
+        const int c = channel(lane, j, i);
+        return make_float2(c < d ? w[c] : 0.f, c + STEP < d ? w[c + STEP] : 0.f);
+    }
+    static __device__ __forceinline__ void put_weight(float* w, int lane, int j, int i, int d,
+                                                      float2 v) {
+        const int c = channel(lane, j, i);
+        if (c < d) w[c] = v.x;
+        if (c + STEP < d) w[c + STEP] = v.y;
+    }
+    // zero what lies outside the group
+    static __device__ __forceinline__ float2 inside(float2 v, int lane, int j, int i, int d) {
+        const int c = channel(lane, j, i);
+        return make_float2(c < d ? v.x : 0.f, c + STEP < d ? v.y : 0.f);
+    }
+};
+
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// sigmoid(a) = 1 / (1 + 2^(-a log2 e)); 0 and 1 far out
+__device__ __forceinline__ float2 sigmoid2(float2 a) {
+    const float2 t = mul2(a, both(-1.4426950408889634f));
+    float2 e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+    e = add2(e, both(1.f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
+    return s;
+}
 
 template <int LG>
 __device__ __forceinline__ float group_sum(float v) {
@@ -97,15 +143,15 @@ __device__ __forceinline__ float group_sum(float v) {
 template <int LG>
 struct Place {
     int lane, head, trips;
-    int64_t row;
+    int64_t row, group;
     bool active;
     __device__ __forceinline__ explicit Place(const NormParams& p) {
         constexpr int GPB = NT / LG;
         lane = threadIdx.x % LG;
-        const int64_t g = (int64_t)blockIdx.x * GPB + threadIdx.x / LG;
-        active = g < (int64_t)p.streams * p.H;
-        head = (int)(g % p.H);
-        row = g / p.H;
+        group = (int64_t)blockIdx.x * GPB + threadIdx.x / LG;
+        active = group < (int64_t)p.streams * p.H;
+        head = (int)(group % p.H);
+        row = group / p.H;
         // the whole warp makes the trips of its first lane group, which has the most
         const int64_t g0 = (int64_t)blockIdx.x * GPB + (threadIdx.x & ~31) / LG;
         const int64_t row0 = g0 / p.H;
@@ -116,220 +162,251 @@ struct Place {
 };
 
 // xh and 1 / sqrt(...) of one group, from its channels in v (zeros outside it).
-template <int LG, int NV, int VE>
-__device__ __forceinline__ float normalise(float (&v)[NV][VE], int lane, int nvec, bool centred,
+template <typename V, int LG, int NV>
+__device__ __forceinline__ float normalise(float2 (&v)[NV][V::NP], int lane, int d, bool centred,
                                            float inv_d, float eps) {
     if (centred) {
-        float s = 0.f;
+        float2 s = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) s += v[j][i];
-        const float m = group_sum<LG>(s) * inv_d;
+            for (int i = 0; i < V::NP; ++i) s = add2(s, v[j][i]);
+        const float2 m = both(-group_sum<LG>(s.x + s.y) * inv_d);
 #pragma unroll
         for (int j = 0; j < NV; ++j)
-            if (lane + LG * j < nvec)
 #pragma unroll
-                for (int i = 0; i < VE; ++i) v[j][i] -= m;
+            for (int i = 0; i < V::NP; ++i)
+                v[j][i] = V::inside(add2(v[j][i], m), lane, j, i, d);
     }
-    float ss = 0.f;
+    float2 ss = both(0.f);
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VE; ++i) ss = fmaf(v[j][i], v[j][i], ss);
-    const float r = rsqrtf(fmaf(group_sum<LG>(ss), inv_d, eps));
+        for (int i = 0; i < V::NP; ++i) ss = fma2(v[j][i], v[j][i], ss);
+    const float r = rsqrtf(fmaf(group_sum<LG>(ss.x + ss.y), inv_d, eps));
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VE; ++i) v[j][i] *= r;
+        for (int i = 0; i < V::NP; ++i) v[j][i] = mul2(v[j][i], both(r));
     return r;
 }
 
-template <typename IO, int VE, int LG, int NV, bool GATED>
-__global__ void __launch_bounds__(NT) group_norm_kernel(const NormParams p) {
+// PLAIN: RMS without bias, the common form; it saves the bias's registers.
+template <typename IO, bool WIDE, int LG, int NV, bool GATED, bool PLAIN>
+__global__ void __launch_bounds__(NT, NV == 1 ? fwd_blocks(GATED, PLAIN) : 1)
+    group_norm_kernel(const NormParams p) {
+    using V = Vec<IO, WIDE, LG>;
     const Place<LG> at(p);
-    float w[NV][VE], b[NV][VE];
-    const int wo = p.per_head ? at.head * p.d : 0;
+    const int lane = at.lane, d = p.d;
+    float2 w[NV][V::NP], b[NV][V::NP];
+    const int wo = p.per_head ? at.head * d : 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            const int vec = at.lane + LG * j;
-            const bool in = vec < p.nvec;
-            w[j][i] = in ? p.w[wo + vec * VE + i] : 0.f;
-            b[j][i] = in && p.has_bias ? p.b[wo + vec * VE + i] : 0.f;
+        for (int i = 0; i < V::NP; ++i) {
+            w[j][i] = V::weight(p.w + wo, lane, j, i, d);
+            b[j][i] = !PLAIN && p.has_bias ? V::weight(p.b + wo, lane, j, i, d) : both(0.f);
         }
-    const int col = at.head * p.d + at.lane * VE;
+    const int64_t col = (int64_t)at.head * d;
+    const IO* px = static_cast<const IO*>(p.x) + at.row * p.xs + col;
+    const IO* pz = GATED ? static_cast<const IO*>(p.z) + at.row * p.zs + col : nullptr;
+    IO* py = static_cast<IO*>(p.y) + at.row * p.ys + col;
+    const int64_t sx = p.streams * p.xs, sz = p.streams * p.zs, sy = p.streams * p.ys;
     int64_t row = at.row;
-    for (int it = 0; it < at.trips; ++it, row += p.streams) {
-        const bool ok = at.active && row < p.T;
-        float v[NV][VE], g[NV][VE];
+    typename V::Raw xr[NV], zr[NV];
+    const auto fetch = [&](bool ok) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const bool in = ok && at.lane + LG * j < p.nvec;
-#pragma unroll
-            for (int i = 0; i < VE; ++i) v[j][i] = 0.f, g[j][i] = 0.f;
-            if (in) {
-                Chan<IO, VE>::load(static_cast<const IO*>(p.x) + row * p.xs + col + LG * VE * j,
-                                   v[j]);
-                if (GATED)
-                    Chan<IO, VE>::load(
-                        static_cast<const IO*>(p.z) + row * p.zs + col + LG * VE * j, g[j]);
-            }
+            xr[j] = V::load(px, lane, j, d, ok);
+            if (GATED) zr[j] = V::load(pz, lane, j, d, ok);
         }
-        normalise<LG>(v, at.lane, p.nvec, p.centred, p.inv_d, ok ? p.eps : 1.f);
+        px += sx;
+        if (GATED) pz += sz;
+    };
+    fetch(at.active && row < p.T);
+    for (int it = 0; it < at.trips; ++it, row += p.streams, py += sy) {
+        const bool ok = at.active && row < p.T;
+        float2 v[NV][V::NP], g[NV][V::NP];
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+            for (int i = 0; i < V::NP; ++i) {
+                v[j][i] = V::pair(xr[j], i);
+                if (GATED) g[j][i] = V::pair(zr[j], i);
+            }
+        fetch(at.active && row + p.streams < p.T);
+        normalise<V, LG, NV>(v, lane, d, !PLAIN && p.centred, p.inv_d, ok ? p.eps : 1.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                const float n = fmaf(v[j][i], w[j][i], b[j][i]);
-                const float a = GATED ? g[j][i] : n;
-                const float s = p.silu ? a * sigmoid_fast(a) : a;
-                v[j][i] = GATED ? n * s : s;
+            for (int i = 0; i < V::NP; ++i) {
+                const float2 n = PLAIN ? mul2(v[j][i], w[j][i]) : fma2(v[j][i], w[j][i], b[j][i]);
+                float2 a = GATED ? g[j][i] : n;
+                if (p.silu) a = mul2(a, sigmoid2(a));
+                v[j][i] = GATED ? mul2(n, a) : a;
             }
-            if (ok && at.lane + LG * j < p.nvec)
-                Chan<IO, VE>::store(static_cast<IO*>(p.y) + row * p.ys + col + LG * VE * j, v[j]);
+            V::store(py, lane, j, d, ok, v[j]);
         }
     }
 }
 
-template <typename IO, int VE, int LG, int NV, bool GATED>
-__global__ void __launch_bounds__(NT) group_norm_backward_kernel(const NormParams p) {
+template <typename IO, bool WIDE, int LG, int NV, bool GATED, bool PLAIN>
+__global__ void __launch_bounds__(NT, NV == 1 ? bwd_blocks(PLAIN, WIDE && sizeof(IO) == 2) : 1)
+    group_norm_backward_kernel(const NormParams p) {
+    using V = Vec<IO, WIDE, LG>;
     constexpr int GPB = NT / LG;
     extern __shared__ float part[];  // [GPB][d], for the sums over a block's groups
     const Place<LG> at(p);
-    float w[NV][VE], b[NV][VE], dw[NV][VE], db[NV][VE];
-    const int wo = p.per_head ? at.head * p.d : 0;
+    const int lane = at.lane, d = p.d;
+    float2 w[NV][V::NP], b[NV][V::NP], dw[NV][V::NP], db[NV][V::NP];
+    const int wo = p.per_head ? at.head * d : 0;
 #pragma unroll
     for (int j = 0; j < NV; ++j)
 #pragma unroll
-        for (int i = 0; i < VE; ++i) {
-            const int vec = at.lane + LG * j;
-            const bool in = vec < p.nvec;
-            w[j][i] = in ? p.w[wo + vec * VE + i] : 0.f;
-            b[j][i] = in && p.has_bias ? p.b[wo + vec * VE + i] : 0.f;
-            dw[j][i] = db[j][i] = 0.f;
+        for (int i = 0; i < V::NP; ++i) {
+            w[j][i] = V::weight(p.w + wo, lane, j, i, d);
+            b[j][i] = !PLAIN && p.has_bias ? V::weight(p.b + wo, lane, j, i, d) : both(0.f);
+            dw[j][i] = db[j][i] = both(0.f);
         }
-    const int col = at.head * p.d + at.lane * VE;
+    const int64_t col = (int64_t)at.head * d;
+    const IO* px = static_cast<const IO*>(p.x) + at.row * p.xs + col;
+    const IO* pd = static_cast<const IO*>(p.dy) + at.row * p.dys + col;
+    const IO* pz = GATED ? static_cast<const IO*>(p.z) + at.row * p.zs + col : nullptr;
+    IO* py = static_cast<IO*>(p.y) + at.row * p.ys + col;
+    IO* pg = GATED ? static_cast<IO*>(p.dz) + at.row * p.dzs + col : nullptr;
+    const int64_t sx = p.streams * p.xs, sd = p.streams * p.dys, sz = p.streams * p.zs;
+    const int64_t sy = p.streams * p.ys, sg = p.streams * p.dzs;
     int64_t row = at.row;
-    for (int it = 0; it < at.trips; ++it, row += p.streams) {
+    typename V::Raw xr[NV], dr[NV], zr[NV];
+    const auto fetch = [&](bool ok) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            xr[j] = V::load(px, lane, j, d, ok);
+            dr[j] = V::load(pd, lane, j, d, ok);
+            if (GATED) zr[j] = V::load(pz, lane, j, d, ok);
+        }
+        px += sx;
+        pd += sd;
+        if (GATED) pz += sz;
+    };
+    fetch(at.active && row < p.T);
+    for (int it = 0; it < at.trips; ++it, row += p.streams, py += sy) {
         const bool ok = at.active && row < p.T;
-        float v[NV][VE], g[NV][VE], dn[NV][VE];
+        float2 v[NV][V::NP], g[NV][V::NP], dn[NV][V::NP];
 #pragma unroll
-        for (int j = 0; j < NV; ++j) {
-            const bool in = ok && at.lane + LG * j < p.nvec;
+        for (int j = 0; j < NV; ++j)
 #pragma unroll
-            for (int i = 0; i < VE; ++i) v[j][i] = 0.f, g[j][i] = 0.f, dn[j][i] = 0.f;
-            if (in) {
-                const int c = col + LG * VE * j;
-                Chan<IO, VE>::load(static_cast<const IO*>(p.x) + row * p.xs + c, v[j]);
-                Chan<IO, VE>::load(static_cast<const IO*>(p.dy) + row * p.dys + c, dn[j]);
-                if (GATED) Chan<IO, VE>::load(static_cast<const IO*>(p.z) + row * p.zs + c, g[j]);
+            for (int i = 0; i < V::NP; ++i) {
+                v[j][i] = V::pair(xr[j], i);
+                dn[j][i] = V::pair(dr[j], i);
+                if (GATED) g[j][i] = V::pair(zr[j], i);
             }
-        }
+        fetch(at.active && row + p.streams < p.T);
         // (a lane group past the last token adds exact zeros to its sums)
-        const float r =
-            normalise<LG>(v, at.lane, p.nvec, p.centred, p.inv_d, ok ? p.eps : 1.f);
-        float se = 0.f, sx = 0.f;
+        const float r = normalise<V, LG, NV>(v, lane, d, !PLAIN && p.centred, p.inv_d,
+                                             ok ? p.eps : 1.f);
+        float2 se = both(0.f), sx2 = both(0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) {
-                const float n = fmaf(v[j][i], w[j][i], b[j][i]);
-                const float a = GATED ? g[j][i] : n;
-                float value = a, slope = 1.f;
+            for (int i = 0; i < V::NP; ++i) {
+                const float2 n = PLAIN ? mul2(v[j][i], w[j][i]) : fma2(v[j][i], w[j][i], b[j][i]);
+                const float2 a = GATED ? g[j][i] : n;
+                float2 value = a, slope = both(1.f);
                 if (p.silu) {
-                    const float s = sigmoid_fast(a);
-                    value = a * s;
-                    slope = fmaf(value, 1.f - s, s);
+                    const float2 s = sigmoid2(a);
+                    value = mul2(a, s);
+                    slope = fma2(value, fma2(s, both(-1.f), both(1.f)), s);
                 }
-                const float dy = dn[j][i];
+                const float2 dy = dn[j][i];
                 if (GATED) {
-                    g[j][i] = dy * n * slope;
-                    dn[j][i] = dy * value;
+                    g[j][i] = mul2(mul2(dy, n), slope);
+                    dn[j][i] = mul2(dy, value);
                 } else {
-                    dn[j][i] = dy * slope;
+                    dn[j][i] = mul2(dy, slope);
                 }
-                dw[j][i] = fmaf(dn[j][i], v[j][i], dw[j][i]);
-                db[j][i] += dn[j][i];
-                dn[j][i] *= w[j][i];
-                se += dn[j][i];
-                sx = fmaf(dn[j][i], v[j][i], sx);
+                dw[j][i] = fma2(dn[j][i], v[j][i], dw[j][i]);
+                if (!PLAIN) db[j][i] = add2(db[j][i], dn[j][i]);
+                dn[j][i] = mul2(dn[j][i], w[j][i]);
+                if (!PLAIN) se = add2(se, dn[j][i]);
+                sx2 = fma2(dn[j][i], v[j][i], sx2);
             }
-            if (GATED && ok && at.lane + LG * j < p.nvec)
-                Chan<IO, VE>::store(static_cast<IO*>(p.dz) + row * p.dzs + col + LG * VE * j, g[j]);
+            if (GATED) V::store(pg, lane, j, d, ok, g[j]);
         }
-        const float cx = group_sum<LG>(sx) * p.inv_d;
-        const float ce = p.centred ? group_sum<LG>(se) * p.inv_d : 0.f;
+        const float2 cx = both(-group_sum<LG>(sx2.x + sx2.y) * p.inv_d);
+        const float2 ce =
+            both(!PLAIN && p.centred ? -group_sum<LG>(se.x + se.y) * p.inv_d : 0.f);
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
 #pragma unroll
-            for (int i = 0; i < VE; ++i) v[j][i] = r * (dn[j][i] - ce - v[j][i] * cx);
-            if (ok && at.lane + LG * j < p.nvec)
-                Chan<IO, VE>::store(static_cast<IO*>(p.y) + row * p.ys + col + LG * VE * j, v[j]);
+            for (int i = 0; i < V::NP; ++i) {
+                float2 e = fma2(v[j][i], cx, dn[j][i]);
+                if (!PLAIN) e = add2(e, ce);
+                v[j][i] = mul2(e, both(r));
+            }
+            V::store(py, lane, j, d, ok, v[j]);
         }
+        if (GATED) pg += sg;
     }
 
     // partial sums: one row per stream of a head, or one row per block
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
+    for (int which = 0; which < (PLAIN ? 1 : 2); ++which) {
         float* out = which ? p.db_part : p.dw_part;
         if (!out) continue;
         if (p.per_head) {
             if (at.active) {
-                const int64_t g = (int64_t)blockIdx.x * GPB + threadIdx.x / LG;
-                float* o = out + (g / p.H) * ((int64_t)p.H * p.d) + at.head * p.d;
+                float* o = out + (at.group / p.H) * ((int64_t)p.H * d) + col;
 #pragma unroll
                 for (int j = 0; j < NV; ++j)
 #pragma unroll
-                    for (int i = 0; i < VE; ++i)
-                        if (at.lane + LG * j < p.nvec)
-                            o[(at.lane + LG * j) * VE + i] = which ? db[j][i] : dw[j][i];
+                    for (int i = 0; i < V::NP; ++i)
+                        V::put_weight(o, lane, j, i, d, which ? db[j][i] : dw[j][i]);
             }
         } else {
-            float* mine = part + (threadIdx.x / LG) * p.d;
+            float* mine = part + (threadIdx.x / LG) * d;
             __syncthreads();
 #pragma unroll
             for (int j = 0; j < NV; ++j)
 #pragma unroll
-                for (int i = 0; i < VE; ++i)
-                    if (at.lane + LG * j < p.nvec)
-                        mine[(at.lane + LG * j) * VE + i] = which ? db[j][i] : dw[j][i];
+                for (int i = 0; i < V::NP; ++i)
+                    V::put_weight(mine, lane, j, i, d, which ? db[j][i] : dw[j][i]);
             __syncthreads();
-            for (int c = threadIdx.x; c < p.d; c += NT) {
+            for (int c = threadIdx.x; c < d; c += NT) {
                 float s = 0.f;
-                for (int q = 0; q < GPB; ++q) s += part[q * p.d + c];
-                out[(int64_t)blockIdx.x * p.d + c] = s;
+                for (int q = 0; q < GPB; ++q) s += part[q * d + c];
+                out[(int64_t)blockIdx.x * d + c] = s;
             }
         }
     }
 }
 
 // Column sums of part [rows, cols] into out (blockIdx.y: the first pair, then the
-// second), in an order that does not depend on timing.
-__global__ void __launch_bounds__(256)
+// second), in an order that does not depend on timing.  Bound by the latency of its
+// loads: 32 rows at once per block, eight of them in flight per thread.
+__global__ void __launch_bounds__(1024)
     column_sums_kernel(const float* part0, const float* part1, float* out0, float* out1, int rows,
                        int cols) {
-    __shared__ float sm[8][33];
+    __shared__ float sm[32][33];
     const float* part = blockIdx.y ? part1 : part0;
     float* out = blockIdx.y ? out1 : out0;
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + tx;
     float s = 0.f;
     if (c < cols)
-#pragma unroll 4
-        for (int r = ty; r < rows; r += 8) s += part[(int64_t)r * cols + c];
+#pragma unroll 8
+        for (int r = ty; r < rows; r += 32) s += part[(int64_t)r * cols + c];
     sm[ty][tx] = s;
     __syncthreads();
-    if (ty == 0 && c < cols) {
+    s = sm[tx][ty];  // warp ty adds column ty
 #pragma unroll
-        for (int q = 1; q < 8; ++q) s += sm[q][tx];
-        out[c] = s;
-    }
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (tx == 0 && blockIdx.x * 32 + ty < cols) out[blockIdx.x * 32 + ty] = s;
 }
 
+// Lanes of a group: a power of two that its vectors fill, 4 to 32.
 int lanes_for(int nvec) {
-    int lg = 1;
+    int lg = 4;
     while (lg < 32 && lg < nvec) lg *= 2;
     return lg;
 }
@@ -338,83 +415,86 @@ int lanes_for(int nvec) {
 struct Shape {
     int lg, blocks, streams;
 };
-Shape shape_of(int T, int H, int nvec, int blocks_per_sm) {
+Shape shape_of(int T, int H, int d, bool wide, bool bf16, int blocks_per_sm, int tokens) {
     Shape s;
-    s.lg = lanes_for(nvec);
+    s.lg = wide ? lanes_for(d / (bf16 ? 8 : 4)) : 32;
     const long long gpb = NT / s.lg, groups = (long long)T * H;
-    const long long need = (groups + gpb - 1) / gpb, least = (H + gpb - 1) / gpb;
+    const long long need = (groups + gpb * tokens - 1) / (gpb * tokens);
+    const long long least = (H + gpb - 1) / gpb;
     long long blocks = (long long)device_sms() * blocks_per_sm;
-    if (blocks < least) blocks = least;
     if (blocks > need) blocks = need;
+    if (blocks < least) blocks = least;
     s.blocks = (int)blocks;
     s.streams = (int)(blocks * gpb / H);
     if (s.streams > T) s.streams = T;
     return s;
 }
 
-template <typename IO, int VE, int LG, int NV>
+bool is_plain(const NormParams& p) { return !p.centred && !p.has_bias; }
+Shape backward_shape(int T, int H, int d, bool wide, bool bf16, bool plain) {
+    return shape_of(T, H, d, wide, bf16, bwd_blocks(plain, wide && bf16), BWD_TOKENS);
+}
+
+template <typename IO, bool WIDE, int LG, int NV, bool GATED, bool PLAIN>
 void launch_one(const NormParams& p, int blocks, bool backward, cudaStream_t stream) {
     if (backward) {
         const size_t smem = p.per_head ? 0 : (size_t)(NT / LG) * p.d * sizeof(float);
-        if (p.z)
-            group_norm_backward_kernel<IO, VE, LG, NV, true><<<blocks, NT, smem, stream>>>(p);
-        else
-            group_norm_backward_kernel<IO, VE, LG, NV, false><<<blocks, NT, smem, stream>>>(p);
+        group_norm_backward_kernel<IO, WIDE, LG, NV, GATED, PLAIN><<<blocks, NT, smem, stream>>>(p);
     } else {
-        if (p.z)
-            group_norm_kernel<IO, VE, LG, NV, true><<<blocks, NT, 0, stream>>>(p);
-        else
-            group_norm_kernel<IO, VE, LG, NV, false><<<blocks, NT, 0, stream>>>(p);
+        group_norm_kernel<IO, WIDE, LG, NV, GATED, PLAIN><<<blocks, NT, 0, stream>>>(p);
     }
 }
 
-template <typename IO, int VE>
-cudaError_t launch_ve(NormParams p, int blocks_per_sm, bool backward, cudaStream_t stream) {
-    p.nvec = p.d / VE;
-    const Shape s = shape_of(p.T, p.H, p.nvec, blocks_per_sm);
+template <typename IO, bool WIDE, int LG, int NV>
+void launch_form(const NormParams& p, int blocks, bool backward, cudaStream_t stream) {
+    const bool plain = is_plain(p);
+    if (p.z)
+        plain ? launch_one<IO, WIDE, LG, NV, true, true>(p, blocks, backward, stream)
+              : launch_one<IO, WIDE, LG, NV, true, false>(p, blocks, backward, stream);
+    else
+        plain ? launch_one<IO, WIDE, LG, NV, false, true>(p, blocks, backward, stream)
+              : launch_one<IO, WIDE, LG, NV, false, false>(p, blocks, backward, stream);
+}
+
+template <typename IO, bool WIDE>
+cudaError_t launch_io(NormParams p, bool backward, cudaStream_t stream) {
+    const Shape s = backward ? backward_shape(p.T, p.H, p.d, WIDE, sizeof(IO) == 2, is_plain(p))
+                             : shape_of(p.T, p.H, p.d, WIDE, sizeof(IO) == 2,
+                                        fwd_blocks(p.z != nullptr, is_plain(p)), 1);
     p.streams = s.streams;
-    constexpr int MAXNV = GDN_MAX_GROUP_DIM / VE / 32;
-    switch (s.lg) {
-        case 1: launch_one<IO, VE, 1, 1>(p, s.blocks, backward, stream); break;
-        case 2: launch_one<IO, VE, 2, 1>(p, s.blocks, backward, stream); break;
-        case 4: launch_one<IO, VE, 4, 1>(p, s.blocks, backward, stream); break;
-        case 8: launch_one<IO, VE, 8, 1>(p, s.blocks, backward, stream); break;
-        case 16: launch_one<IO, VE, 16, 1>(p, s.blocks, backward, stream); break;
-        default: {
-            const int nv = (p.nvec + 31) / 32;
-            if (nv <= 1) launch_one<IO, VE, 32, 1>(p, s.blocks, backward, stream);
-            else if (nv <= 2) launch_one<IO, VE, 32, 2>(p, s.blocks, backward, stream);
-            else if (nv <= 4) launch_one<IO, VE, 32, 4>(p, s.blocks, backward, stream);
-            else if constexpr (MAXNV > 4) {
-                if (nv <= 8) launch_one<IO, VE, 32, 8>(p, s.blocks, backward, stream);
-                else if constexpr (MAXNV > 8) {
-                    if (nv <= 16) launch_one<IO, VE, 32, 16>(p, s.blocks, backward, stream);
-                    else launch_one<IO, VE, 32, 32>(p, s.blocks, backward, stream);
-                }
-            }
-        }
+    constexpr int PER = WIDE ? 32 * 16 / (int)sizeof(IO) : 64;  // channels of 32 lanes' vectors
+    const int nv = (p.d + PER - 1) / PER;
+    if (WIDE && s.lg == 4) launch_form<IO, WIDE, 4, 1>(p, s.blocks, backward, stream);
+    else if (WIDE && s.lg == 8) launch_form<IO, WIDE, 8, 1>(p, s.blocks, backward, stream);
+    else if (WIDE && s.lg == 16) launch_form<IO, WIDE, 16, 1>(p, s.blocks, backward, stream);
+    else if (nv <= 1) launch_form<IO, WIDE, 32, 1>(p, s.blocks, backward, stream);
+    else if (nv <= 2) launch_form<IO, WIDE, 32, 2>(p, s.blocks, backward, stream);
+    else if (nv <= 4) launch_form<IO, WIDE, 32, 4>(p, s.blocks, backward, stream);
+    else if constexpr (GDN_MAX_GROUP_DIM > 4 * PER) {
+        if (nv <= 8) launch_form<IO, WIDE, 32, 8>(p, s.blocks, backward, stream);
+        else if constexpr (GDN_MAX_GROUP_DIM > 8 * PER)
+            launch_form<IO, WIDE, 32, 16>(p, s.blocks, backward, stream);
     }
     return cudaGetLastError();
 }
 
-// Channels per access: 16 bytes where every pointer, stride and the group allow it, else one.
-int vector_of(const NormParams& p, bool bf16) {
+// Whether every pointer, stride and the group itself allow 16-byte accesses.
+bool wide_norm(const NormParams& p, bool bf16) {
     const int ve = bf16 ? 8 : 4;
     const void* ptrs[] = {p.x, p.z, p.dy, p.y, p.dz};
     const int64_t strides[] = {p.xs, p.zs, p.dys, p.ys, p.dzs};
-    if (p.d % ve) return 1;
+    if (p.d % ve) return false;
     for (int i = 0; i < 5; ++i)
-        if (ptrs[i] && (reinterpret_cast<uintptr_t>(ptrs[i]) % 16 || strides[i] % ve)) return 1;
-    return ve;
+        if (ptrs[i] && (reinterpret_cast<uintptr_t>(ptrs[i]) % 16 || strides[i] % ve)) return false;
+    return true;
 }
 
-cudaError_t launch_any(const NormParams& p, bool bf16, int blocks_per_sm, bool backward,
-                       cudaStream_t stream) {
-    if (vector_of(p, bf16) > 1)
-        return bf16 ? launch_ve<__nv_bfloat16, 8>(p, blocks_per_sm, backward, stream)
-                    : launch_ve<float, 4>(p, blocks_per_sm, backward, stream);
-    return bf16 ? launch_ve<__nv_bfloat16, 1>(p, blocks_per_sm, backward, stream)
-                : launch_ve<float, 1>(p, blocks_per_sm, backward, stream);
+cudaError_t launch_any(const NormParams& p, bool bf16, bool backward, cudaStream_t stream) {
+    if (wide_norm(p, bf16))
+        return bf16 ? launch_io<__nv_bfloat16, true>(p, backward, stream)
+                    : launch_io<float, true>(p, backward, stream);
+    return bf16 ? launch_io<__nv_bfloat16, false>(p, backward, stream)
+                : launch_io<float, false>(p, backward, stream);
 }
 
 NormParams params_of(const GroupNormArgs& a) {
@@ -430,8 +510,8 @@ NormParams params_of(const GroupNormArgs& a) {
 
 // Rows of partial sums that the backward kernel writes: one per stream (weights
 // per head) or one per block.
-int partial_rows(int T, int H, int d, bool per_head, int ve) {
-    const Shape s = shape_of(T, H, d / ve, BWD_BLOCKS);
+int partial_rows(int T, int H, int d, bool per_head, bool wide, bool bf16, bool plain) {
+    const Shape s = backward_shape(T, H, d, wide, bf16, plain);
     return per_head ? s.streams : s.blocks;
 }
 
@@ -439,25 +519,25 @@ int partial_rows(int T, int H, int d, bool per_head, int ve) {
 
 cudaError_t launch_column_sums(const float* part0, const float* part1, float* out0, float* out1,
                                int rows, int cols, cudaStream_t stream) {
-    column_sums_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 256, 0, stream>>>(
+    column_sums_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 1024, 0, stream>>>(
         part0, part1, out0, out1, rows, cols);
     return cudaGetLastError();
 }
 
 cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream) {
     if (a.T == 0) return cudaSuccess;
-    return launch_any(params_of(a), a.bf16, FWD_BLOCKS, false, stream);
+    return launch_any(params_of(a), a.bf16, false, stream);
 }
 
 size_t group_norm_backward_workspace_bytes(int T, int H, int d, int weight_heads, bool bf16) {
     if (T == 0) return 0;
     const bool per_head = weight_heads != 1;
     const size_t cols = (size_t)(per_head ? H : 1) * d;
-    // enough for either access width: the pointers are not known here
+    // enough for every form of the call: pointers, bias and norm are not known here
     size_t rows = 0;
-    for (const int ve : {bf16 ? 8 : 4, 1})
-        if (d % ve == 0) {
-            const size_t r = (size_t)partial_rows(T, H, d, per_head, ve);
+    for (const bool wide : {false, true})
+        for (const bool plain : {false, true}) {
+            const size_t r = (size_t)partial_rows(T, H, d, per_head, wide, bf16, plain);
             rows = r > rows ? r : rows;
         }
     return 2 * ((rows * cols * sizeof(float) + 255) / 256 * 256);
@@ -474,9 +554,9 @@ cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, f
             group_norm_backward_workspace_bytes(a.T, a.H, a.d, a.weight_heads, a.bf16) / 2;
         p.dw_part = static_cast<float*>(workspace);
         if (dbias) p.db_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + half);
-        const cudaError_t e = launch_any(p, a.bf16, BWD_BLOCKS, true, stream);
+        const cudaError_t e = launch_any(p, a.bf16, true, stream);
         if (e != cudaSuccess) return e;
-        rows = partial_rows(a.T, a.H, a.d, per_head, vector_of(p, a.bf16));
+        rows = partial_rows(a.T, a.H, a.d, per_head, wide_norm(p, a.bf16), a.bf16, is_plain(p));
     }
     return launch_column_sums(p.dw_part, p.db_part, dweight, dbias, rows, cols, stream);
 }
