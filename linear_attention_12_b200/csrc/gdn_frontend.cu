@@ -317,27 +317,215 @@ __global__ void __launch_bounds__(32)
 // a rolling window of three raw rows feeds the convolution, three partial rows of dx
 // wait for the tokens ahead of them, and dw runs in registers.  Runs overlap by the
 // three rows behind and ahead of them.
+//
+// Every warp keeps FG_STAGES tiles of FG_ROWS rows (x and the output gradient) on their
+// way by TMA into its own part of shared memory, and takes four rows at a time: their
+// activations, and for q and k the two sums over the head, do not depend on one another, so
+// their latencies overlap.  The arithmetic goes two channels to an instruction (about 14 per
+// channel of v and 23 of q and k instead of 28 and 40).
+constexpr int FG_WARPS = 4;         // per block, each on its own
+constexpr int FG_BLOCKS = 4;        // blocks per SM, all runs at once
+constexpr int FG_STAGES = 3;
+constexpr int FG_STAGE_BYTES = 4096;  // of a warp: FG_ROWS rows of x, as many of the gradient
+template <typename IO>
+__host__ __device__ constexpr int fg_rows() { return FG_STAGE_BYTES / (2 * FD * (int)sizeof(IO)); }
+constexpr int FG_SMEM = FG_WARPS * FG_STAGES * (FG_STAGE_BYTES + 8) + 16;
+
 struct FrontendGradParams {
     FrontendGradArgs a;
     float* part;  // [runs, (2 H_qk + H_v) d, 4] partial sums of dw
     int runs, run_len, blocks;  // blocks of the convolution part; the rest take the gates
 };
+struct FrontendGradMaps {
+    CUtensorMap x[3], dout[3];
+};
 
-__device__ __forceinline__ float4 fma4(float4 a, float4 b, float4 c) {
-    return make_float4(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y), fmaf(a.z, b.z, c.z),
-                       fmaf(a.w, b.w, c.w));
+// Four channels as two pairs.
+struct F4 {
+    float2 lo, hi;
+};
+__device__ __forceinline__ F4 zero4() { return F4{both(0.f), both(0.f)}; }
+__device__ __forceinline__ F4 fma4(const F4& a, const F4& b, const F4& c) {
+    return F4{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
 }
-__device__ __forceinline__ float4 mul4(float4 a, float4 b) {
-    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+__device__ __forceinline__ F4 mul4(const F4& a, const F4& b) {
+    return F4{mul2(a.lo, b.lo), mul2(a.hi, b.hi)};
 }
-__device__ __forceinline__ float dot4(float4 a, float4 b) {
-    return fmaf(a.x, b.x, fmaf(a.y, b.y, fmaf(a.z, b.z, a.w * b.w)));
+__device__ __forceinline__ float dot4(const F4& a, const F4& b) {
+    const float2 s = fma2(a.hi, b.hi, mul2(a.lo, b.lo));
+    return s.x + s.y;
+}
+template <typename IO>
+__device__ __forceinline__ F4 load4(const IO* p) {
+    const float4 v = Vec4<IO>::load(p);
+    return F4{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+}
+template <typename IO>
+__device__ __forceinline__ void store4(IO* p, const F4& v) {
+    Vec4<IO>::store(p, make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y));
 }
 
-constexpr int FG_WARPS = 4;
+// What a warp carries from row to row.
+struct GradState {
+    F4 w[4], dw[4];
+    F4 x1, x2, x3;  // raw rows t - 1, t - 2, t - 3 (zeros before the sequence)
+    F4 d1, d2, d3;  // dx of tokens t - 1, t - 2, t - 3 so far
+    int lo;         // the first token whose dx is pending or stored here
+};
+
+// Rows t .. t + NR - 1 of one sequence: x and dout at xs, gs (rows `pitch` elements apart);
+// dx of tokens t - 3 .. t + NR - 4 is complete after it and stored.
+template <int NR, bool L2, bool SILU, bool DW, typename IO>
+__device__ __forceinline__ void grad_rows(GradState& s, int t, const IO* xs, const IO* gs,
+                                          int64_t pitch, IO* dx, int64_t rs, float eps) {
+    F4 x[NR + 3], u[NR], slope[NR], dy[NR];
+    x[0] = s.x3, x[1] = s.x2, x[2] = s.x1;
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        x[i + 3] = load4(xs + i * pitch);
+        dy[i] = load4(gs + i * pitch);
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        const F4 y = fma4(s.w[0], x[i], fma4(s.w[1], x[i + 1],
+                                              fma4(s.w[2], x[i + 2], mul4(s.w[3], x[i + 3]))));
+        u[i] = y;
+        if (SILU) {
+            const F4 g{sigmoid2(y.lo), sigmoid2(y.hi)};
+            u[i] = mul4(y, g);
+            slope[i] = F4{fma2(u[i].lo, fma2(g.lo, both(-1.f), both(1.f)), g.lo),
+                          fma2(u[i].hi, fma2(g.hi, both(-1.f), both(1.f)), g.hi)};
+        }
+    }
+    if (L2) {
+        float ss[NR], ud[NR];
+#pragma unroll
+        for (int i = 0; i < NR; ++i) ss[i] = dot4(u[i], u[i]), ud[i] = dot4(u[i], dy[i]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
+                ud[i] += __shfl_xor_sync(0xffffffffu, ud[i], o);
+            }
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            const float r = rsqrtf(ss[i] + eps);
+            const float2 r2 = both(r), c = both(-r * r * r * ud[i]);
+            dy[i] = F4{fma2(u[i].lo, c, mul2(r2, dy[i].lo)), fma2(u[i].hi, c, mul2(r2, dy[i].hi))};
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NR; ++i) {
+        if (SILU) dy[i] = mul4(dy[i], slope[i]);
+        if (DW)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s.dw[k] = fma4(dy[i], x[i + k], s.dw[k]);
+        const F4 done = fma4(s.w[0], dy[i], s.d3);
+        if (t + i - 3 >= s.lo) store4(dx + (t + i - 3) * rs, done);
+        s.d3 = fma4(s.w[1], dy[i], s.d2);
+        s.d2 = fma4(s.w[2], dy[i], s.d1);
+        s.d1 = mul4(s.w[3], dy[i]);
+    }
+    s.x3 = x[NR], s.x2 = x[NR + 1], s.x1 = x[NR + 2];
+}
+
+// Nothing follows token t - 1 in its sequence or run: what waits is complete.
+template <typename IO>
+__device__ __forceinline__ void grad_flush(const GradState& s, int t, int tb, IO* dx, int64_t rs) {
+    if (t - 3 >= s.lo && t - 3 < tb) store4(dx + (t - 3) * rs, s.d3);
+    if (t - 2 >= s.lo && t - 2 < tb) store4(dx + (t - 2) * rs, s.d2);
+    if (t - 1 >= s.lo && t - 1 < tb) store4(dx + (t - 1) * rs, s.d1);
+}
+
+template <typename IO, bool SILU, bool L2>
+__device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState& s, const IO* x,
+                                         const IO* go, IO* dx, int64_t rs, int ta, int tb,
+                                         int T_end, const CUtensorMap* mx, const CUtensorMap* mg,
+                                         int c0, uint8_t* ring, uint64_t* full,
+                                         volatile int* abort_flag) {
+    constexpr int ROWS = fg_rows<IO>();
+    const int lane = threadIdx.x & 31;
+    const int tiles = (tb - ta + ROWS - 1) / ROWS;
+    const auto fetch = [&](int i) {
+        if (i >= tiles || lane != 0) return;
+        uint8_t* d = ring + i % FG_STAGES * FG_STAGE_BYTES;
+        uint64_t* bar = &full[i % FG_STAGES];
+        mbar_arrive_expect_tx(bar, FG_STAGE_BYTES);
+        tma_load_2d(d, mx, c0, ta + i * ROWS, bar);
+        tma_load_2d(d + FG_STAGE_BYTES / 2, mg, c0, ta + i * ROWS, bar);
+    };
+    for (int i = 0; i < FG_STAGES; ++i) fetch(i);
+
+    // the sequence of token ta, and where the next one starts
+    int n = 0, first = 0, next = T_end;
+    if (a.cu_seqlens) {
+        int hi = a.N - 1;
+        while (n < hi) {
+            const int mid = (n + hi + 1) >> 1;
+            if (a.cu_seqlens[mid] <= ta) n = mid; else hi = mid - 1;
+        }
+        first = max(a.cu_seqlens[n], 0);
+        next = a.cu_seqlens[n + 1];
+    }
+    s.x1 = ta - 1 >= first ? load4(x + (ta - 1) * rs) : zero4();
+    s.x2 = ta - 2 >= first ? load4(x + (ta - 2) * rs) : zero4();
+    s.x3 = ta - 3 >= first ? load4(x + (ta - 3) * rs) : zero4();
+    s.d1 = s.d2 = s.d3 = zero4();
+    s.lo = max(first, ta);
+    const auto start = [&](int t) {  // a sequence starts at token t
+        grad_flush(s, t, tb, dx, rs);
+        s.x1 = s.x2 = s.x3 = s.d1 = s.d2 = s.d3 = zero4();
+        s.lo = t;
+        do {
+            ++n;
+        } while (n + 1 < a.N && a.cu_seqlens[n + 1] <= t);
+        next = a.cu_seqlens[n + 1];
+    };
+
+    for (int i = 0; i < tiles; ++i) {
+        if (!mbar_wait(&full[i % FG_STAGES], (i / FG_STAGES) & 1, abort_flag)) {
+            // the copies may still land: wait for them (bounded) before the block ends
+            const unsigned long long ts = globaltimer();
+            for (int k = i; k < min(i + FG_STAGES, tiles); ++k)
+                while (!mbar_try_wait(smem_u32(&full[k % FG_STAGES]), (k / FG_STAGES) & 1) &&
+                       globaltimer() - ts < kWaitLimitNs) {
+                }
+            return;
+        }
+        const IO* xs = reinterpret_cast<const IO*>(ring + i % FG_STAGES * FG_STAGE_BYTES) + 4 * lane;
+        const IO* gs = xs + ROWS * FD;
+#pragma unroll 1
+        for (int r = 0; r < ROWS; r += 2) {
+            const int t = ta + i * ROWS + r;
+            if (t >= tb) break;
+            if (t == next) start(t);
+            if (t + 2 <= tb && next >= t + 2) {
+                grad_rows<2, L2, SILU, true>(s, t, xs + r * FD, gs + r * FD, FD, dx, rs, a.eps);
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < 2 && t + k < tb; ++k) {
+                    if (t + k == next) start(t + k);
+                    grad_rows<1, L2, SILU, true>(s, t + k, xs + (r + k) * FD, gs + (r + k) * FD, FD,
+                                                 dx, rs, a.eps);
+                }
+            }
+        }
+        __syncwarp();  // everyone has read the tile
+        fetch(i + FG_STAGES);
+    }
+    // the tokens ahead of the run's last three, for their dx alone
+    const int te = min(tb + 3, T_end);
+    int t = tb;
+#pragma unroll 1
+    for (; t < te && t != next; ++t)
+        grad_rows<1, L2, SILU, false>(s, t, x + t * rs, go + t * rs, rs, dx, rs, a.eps);
+    grad_flush(s, t, tb, dx, rs);
+}
 
 template <typename IO, int ACT>
-__global__ void __launch_bounds__(FG_WARPS * 32) frontend_grad_kernel(const FrontendGradParams p) {
+__global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
+    frontend_grad_kernel(const __grid_constant__ FrontendGradMaps maps, const FrontendGradParams p) {
     const FrontendGradArgs& a = p.a;
     const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
     if ((int)blockIdx.x >= p.blocks) {  // the gates, element by element
@@ -351,7 +539,19 @@ __global__ void __launch_bounds__(FG_WARPS * 32) frontend_grad_kernel(const Fron
         }
         return;
     }
+    extern __shared__ __align__(128) uint8_t fg_sm[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring = fg_sm + warp * FG_STAGES * FG_STAGE_BYTES;
+    uint64_t* full =
+        reinterpret_cast<uint64_t*>(fg_sm + FG_WARPS * FG_STAGES * FG_STAGE_BYTES) + warp * FG_STAGES;
+    volatile int* abort_flag =
+        reinterpret_cast<volatile int*>(fg_sm + FG_WARPS * FG_STAGES * (FG_STAGE_BYTES + 8));
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < FG_STAGES; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
     const int heads = 2 * a.H_qk + a.H_v;
     const int64_t unit = (int64_t)blockIdx.x * FG_WARPS + warp;
     if (unit >= (int64_t)p.runs * heads) return;
@@ -365,114 +565,73 @@ __global__ void __launch_bounds__(FG_WARPS * 32) frontend_grad_kernel(const Fron
         static_cast<const IO*>(kind == 0 ? a.dout[0] : (kind == 1 ? a.dout[1] : a.dout[2])) + off;
     IO* dx = static_cast<IO*>(kind == 0 ? a.dx[0] : (kind == 1 ? a.dx[1] : a.dx[2])) + off;
 
-    const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-    float4 w[4], dw[4] = {z, z, z, z};
+    GradState s;
     {
+        // 4 channels x 4 taps, channel-major -> the taps' pairs of channels
         const float4* wp = reinterpret_cast<const float4*>(a.w + ((int64_t)hid * FD + 4 * lane) * 4);
         const float4 c0 = wp[0], c1 = wp[1], c2 = wp[2], c3 = wp[3];
-        w[0] = make_float4(c0.x, c1.x, c2.x, c3.x);
-        w[1] = make_float4(c0.y, c1.y, c2.y, c3.y);
-        w[2] = make_float4(c0.z, c1.z, c2.z, c3.z);
-        w[3] = make_float4(c0.w, c1.w, c2.w, c3.w);
+        s.w[0] = F4{make_float2(c0.x, c1.x), make_float2(c2.x, c3.x)};
+        s.w[1] = F4{make_float2(c0.y, c1.y), make_float2(c2.y, c3.y)};
+        s.w[2] = F4{make_float2(c0.z, c1.z), make_float2(c2.z, c3.z)};
+        s.w[3] = F4{make_float2(c0.w, c1.w), make_float2(c2.w, c3.w)};
+        for (int k = 0; k < 4; ++k) s.dw[k] = zero4();
     }
-
     const int64_t first = (int64_t)run * p.run_len;
     const int ta = (int)min(first, (int64_t)T_end), tb = (int)min(first + p.run_len, (int64_t)T_end);
     if (ta < tb) {
-        // the sequence of token ta, and where the next one starts
-        int n = 0, s = 0, next = T_end;
-        if (a.cu_seqlens) {
-            int hi = a.N - 1;
-            while (n < hi) {
-                const int mid = (n + hi + 1) >> 1;
-                if (a.cu_seqlens[mid] <= ta) n = mid; else hi = mid - 1;
-            }
-            s = max(a.cu_seqlens[n], 0);
-            next = a.cu_seqlens[n + 1];
-        }
-        float4 x1 = ta - 1 >= s ? Vec4<IO>::load(x + (ta - 1) * rs) : z;
-        float4 x2 = ta - 2 >= s ? Vec4<IO>::load(x + (ta - 2) * rs) : z;
-        float4 x3 = ta - 3 >= s ? Vec4<IO>::load(x + (ta - 3) * rs) : z;
-        float4 d1 = z, d2 = z, d3 = z;  // dx of tokens t - 1, t - 2, t - 3 so far
-        int lo = max(s, ta);            // the first token whose dx is pending or stored here
-        const int te = min(tb + 3, T_end);
-        int t = ta;
-        for (; t < te; ++t) {
-            if (t == next) {  // a sequence starts: what waits has no tokens ahead of it
-                if (t - 3 >= lo && t - 3 < tb) Vec4<IO>::store(dx + (t - 3) * rs, d3);
-                if (t - 2 >= lo && t - 2 < tb) Vec4<IO>::store(dx + (t - 2) * rs, d2);
-                if (t - 1 >= lo && t - 1 < tb) Vec4<IO>::store(dx + (t - 1) * rs, d1);
-                x1 = x2 = x3 = d1 = d2 = d3 = z;
-                lo = t;
-                do {
-                    ++n;
-                } while (n + 1 < a.N && a.cu_seqlens[n + 1] <= t);
-                next = a.cu_seqlens[n + 1];
-                if (t >= tb) break;
-            }
-            const float4 x0 = Vec4<IO>::load(x + t * rs);
-            float4 dy = Vec4<IO>::load(go + t * rs);
-            float4 y = conv4(w, x3, x2, x1, x0), u = y, slope = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (ACT == GDN_ACT_SILU) {
-                const float4 sg =
-                    make_float4(sigmoidf(y.x), sigmoidf(y.y), sigmoidf(y.z), sigmoidf(y.w));
-                u = mul4(y, sg);
-                slope = make_float4(fmaf(u.x, 1.f - sg.x, sg.x), fmaf(u.y, 1.f - sg.y, sg.y),
-                                    fmaf(u.z, 1.f - sg.z, sg.z), fmaf(u.w, 1.f - sg.w, sg.w));
-            }
-            if (kind < 2) {
-                float ss = dot4(u, u), ud = dot4(u, dy);
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) {
-                    ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                    ud += __shfl_xor_sync(0xffffffffu, ud, o);
-                }
-                const float r = rsqrtf(ss + a.eps), c = -r * r * r * ud;
-                dy = make_float4(fmaf(u.x, c, r * dy.x), fmaf(u.y, c, r * dy.y),
-                                 fmaf(u.z, c, r * dy.z), fmaf(u.w, c, r * dy.w));
-            }
-            if (ACT == GDN_ACT_SILU) dy = mul4(dy, slope);
-            if (t < tb) {
-                dw[0] = fma4(dy, x3, dw[0]);
-                dw[1] = fma4(dy, x2, dw[1]);
-                dw[2] = fma4(dy, x1, dw[2]);
-                dw[3] = fma4(dy, x0, dw[3]);
-            }
-            d3 = fma4(w[0], dy, d3);
-            if (t - 3 >= lo) Vec4<IO>::store(dx + (t - 3) * rs, d3);
-            d3 = fma4(w[1], dy, d2);
-            d2 = fma4(w[2], dy, d1);
-            d1 = mul4(w[3], dy);
-            x3 = x2;
-            x2 = x1;
-            x1 = x0;
-        }
-        if (t == te) {  // the end of the run (or of the tokens)
-            if (t - 3 >= lo && t - 3 < tb) Vec4<IO>::store(dx + (t - 3) * rs, d3);
-            if (t - 2 >= lo && t - 2 < tb) Vec4<IO>::store(dx + (t - 2) * rs, d2);
-            if (t - 1 >= lo && t - 1 < tb) Vec4<IO>::store(dx + (t - 1) * rs, d1);
-        }
+        if (kind == 2)
+            grad_run<IO, ACT == GDN_ACT_SILU, false>(a, s, x, go, dx, rs, ta, tb, T_end, &maps.x[2],
+                                                     &maps.dout[2], head * FD, ring, full, abort_flag);
+        else
+            grad_run<IO, ACT == GDN_ACT_SILU, true>(
+                a, s, x, go, dx, rs, ta, tb, T_end, kind == 0 ? &maps.x[0] : &maps.x[1],
+                kind == 0 ? &maps.dout[0] : &maps.dout[1], head * FD, ring, full, abort_flag);
     }
     float4* o = reinterpret_cast<float4*>(p.part) + ((int64_t)run * heads + hid) * FD + 4 * lane;
-    o[0] = make_float4(dw[0].x, dw[1].x, dw[2].x, dw[3].x);
-    o[1] = make_float4(dw[0].y, dw[1].y, dw[2].y, dw[3].y);
-    o[2] = make_float4(dw[0].z, dw[1].z, dw[2].z, dw[3].z);
-    o[3] = make_float4(dw[0].w, dw[1].w, dw[2].w, dw[3].w);
+    o[0] = make_float4(s.dw[0].lo.x, s.dw[1].lo.x, s.dw[2].lo.x, s.dw[3].lo.x);
+    o[1] = make_float4(s.dw[0].lo.y, s.dw[1].lo.y, s.dw[2].lo.y, s.dw[3].lo.y);
+    o[2] = make_float4(s.dw[0].hi.x, s.dw[1].hi.x, s.dw[2].hi.x, s.dw[3].hi.x);
+    o[3] = make_float4(s.dw[0].hi.y, s.dw[1].hi.y, s.dw[2].hi.y, s.dw[3].hi.y);
 }
 
-// Runs per head: enough warps for the SMs, runs of at least 32 tokens.
-int frontend_grad_runs(int T, int heads) {
-    const long long want = ((long long)device_sms() * 24 + heads - 1) / heads;
+// Runs per head: all warps at once, runs of at least 32 tokens, whole tiles of rows.
+struct GradRuns {
+    int runs, len;
+};
+GradRuns frontend_grad_runs(int T, int heads) {
+    const long long warps = (long long)device_sms() * FG_BLOCKS * FG_WARPS;
+    long long runs = warps / heads;
     const long long most = ((long long)T + 31) / 32;
-    const long long r = want < most ? want : most;
-    return (int)(r < 1 ? 1 : r);
+    if (runs > most) runs = most;
+    if (runs < 1) runs = 1;
+    long long len = (T + runs - 1) / runs;
+    len = (len + 7) / 8 * 8;
+    return GradRuns{(int)((T + len - 1) / len), (int)len};
+}
+
+template <typename IO, int ACT>
+cudaError_t launch_frontend_grad(const FrontendGradParams& p, unsigned grid, cudaStream_t stream) {
+    const FrontendGradArgs& a = p.a;
+    FrontendGradMaps maps{};
+    for (int k = 0; k < 3; ++k) {
+        const int64_t C = (int64_t)(k == 2 ? a.H_v : a.H_qk) * FD;
+        if (!tile_map(&maps.x[k], a.x[k], a.bf16, a.T, C, C, FD, fg_rows<IO>()) ||
+            !tile_map(&maps.dout[k], a.dout[k], a.bf16, a.T, C, C, FD, fg_rows<IO>()))
+            return cudaErrorInvalidValue;
+    }
+    const auto kernel = frontend_grad_kernel<IO, ACT>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FG_SMEM);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, FG_WARPS * 32, FG_SMEM, stream>>>(maps, p);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 size_t frontend_backward_workspace_bytes(int T, int H_qk, int H_v) {
     const int heads = 2 * H_qk + H_v;
-    return T == 0 ? 0 : (size_t)frontend_grad_runs(T, heads) * heads * FD * 4 * sizeof(float);
+    return T == 0 ? 0 : (size_t)frontend_grad_runs(T, heads).runs * heads * FD * 4 * sizeof(float);
 }
 
 cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
@@ -482,26 +641,20 @@ cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
     p.a = a;
     p.part = static_cast<float*>(workspace);
     if (a.T > 0) {
-        p.runs = frontend_grad_runs(a.T, heads);
-        p.run_len = (a.T + p.runs - 1) / p.runs;
+        const GradRuns g = frontend_grad_runs(a.T, heads);
+        p.runs = g.runs;
+        p.run_len = g.len;
         const long long blocks = ((long long)p.runs * heads + FG_WARPS - 1) / FG_WARPS;
         const long long gates = ((long long)a.T * a.H_v + 1023) / 1024;  // 8 or more per thread
         const long long gate_blocks = gates < 148 ? gates : 148;
         if (blocks + gate_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
         p.blocks = (int)blocks;
         const unsigned grid = (unsigned)(blocks + gate_blocks);
-        if (a.bf16) {
-            if (a.silu)
-                frontend_grad_kernel<__nv_bfloat16, GDN_ACT_SILU><<<grid, FG_WARPS * 32, 0, stream>>>(p);
-            else
-                frontend_grad_kernel<__nv_bfloat16, GDN_ACT_NONE><<<grid, FG_WARPS * 32, 0, stream>>>(p);
-        } else {
-            if (a.silu)
-                frontend_grad_kernel<float, GDN_ACT_SILU><<<grid, FG_WARPS * 32, 0, stream>>>(p);
-            else
-                frontend_grad_kernel<float, GDN_ACT_NONE><<<grid, FG_WARPS * 32, 0, stream>>>(p);
-        }
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e =
+            a.bf16 ? (a.silu ? launch_frontend_grad<__nv_bfloat16, GDN_ACT_SILU>(p, grid, stream)
+                             : launch_frontend_grad<__nv_bfloat16, GDN_ACT_NONE>(p, grid, stream))
+                   : (a.silu ? launch_frontend_grad<float, GDN_ACT_SILU>(p, grid, stream)
+                             : launch_frontend_grad<float, GDN_ACT_NONE>(p, grid, stream));
         if (e != cudaSuccess) return e;
     }
     return launch_column_sums(p.part, nullptr, a.dw, nullptr, p.runs, heads * FD * 4, stream);

@@ -1,6 +1,7 @@
 // gdn_internal.h -- launchers behind the C ABI (not part of the public header).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -78,6 +79,11 @@ cudaError_t launch_frontend_decode(const void* q_raw, const void* k_raw, const v
                                    void* conv_state, int B, int H_qk, int H_v, bool bf16, int act,
                                    float eps, void* q, void* k, void* v, float* log_alpha,
                                    float* beta, cudaStream_t stream);
+
+// The tensor map of a [T, C] tensor (row stride in elements) read in boxes of rows x cols,
+// rows and columns outside it as zeros; false if the driver refuses it.
+bool tile_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t C, int64_t stride,
+              int cols, int rows);
 
 // The per-channel recurrence (row strides in elements; the step's T is its B and
 // its h_final the state).

@@ -116,20 +116,6 @@ struct Vec {
     }
 };
 
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-
-// sigmoid(a) = 1 / (1 + 2^(-a log2 e)); 0 and 1 far out
-__device__ __forceinline__ float2 sigmoid2(float2 a) {
-    const float2 t = mul2(a, both(-1.4426950408889634f));
-    float2 e, s;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
-    e = add2(e, both(1.f));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.x) : "f"(e.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s.y) : "f"(e.y));
-    return s;
-}
-
 template <int LG>
 __device__ __forceinline__ float group_sum(float v) {
 #pragma unroll

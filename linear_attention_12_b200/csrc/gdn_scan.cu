@@ -555,32 +555,6 @@ __global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs p) {
     }
 }
 
-// A [T, C] tensor as boxes of `rows` x CW; false if the driver refuses it.
-bool tile_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t C, int64_t stride,
-              int rows) {
-    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-    static const Encode encode = [] {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            fn = nullptr;
-        return reinterpret_cast<Encode>(fn);
-    }();
-    if (!encode) return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)T};
-    const cuuint64_t strides[1] = {(cuuint64_t)stride * (bf16 ? 2 : 4)};
-    const cuuint32_t box[2] = {CW, (cuuint32_t)rows}, ones[2] = {1, 1};
-    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
-                  const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool wide_rows(const void* ptr, int64_t stride, int elem) {
     return reinterpret_cast<uintptr_t>(ptr) % 16 == 0 && stride * elem % 16 == 0;
 }
@@ -591,9 +565,9 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     const auto kernel = scan_kernel<IO, G, BWD, TMA, WARPS, ST, MINB>;
     CUtensorMap mx{}, ml{}, mh{};
     if (TMA && p.T > 0) {
-        if (!tile_map(&mx, p.x, sizeof(IO) == 2, p.T, p.C, p.xs, SM::TT) ||
-            !tile_map(&ml, p.la, sizeof(G) == 2, p.T, p.C, p.las, SM::TT) ||
-            (BWD && !tile_map(&mh, p.h, sizeof(IO) == 2, p.T, p.C, p.hs, SM::TT)))
+        if (!tile_map(&mx, p.x, sizeof(IO) == 2, p.T, p.C, p.xs, CW, SM::TT) ||
+            !tile_map(&ml, p.la, sizeof(G) == 2, p.T, p.C, p.las, CW, SM::TT) ||
+            (BWD && !tile_map(&mh, p.h, sizeof(IO) == 2, p.T, p.C, p.hs, CW, SM::TT)))
             return cudaErrorInvalidValue;
     }
     cudaError_t e =
@@ -671,6 +645,31 @@ cudaError_t launch_direction(const ScanParams& p, bool bf16, bool gate_bf16, cud
 }
 
 }  // namespace
+
+bool tile_map(CUtensorMap* map, const void* base, bool bf16, int64_t T, int64_t C, int64_t stride,
+              int cols, int rows) {
+    using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult found = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (!encode) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)C, (cuuint64_t)T};
+    const cuuint64_t strides[1] = {(cuuint64_t)stride * (bf16 ? 2 : 4)};
+    const cuuint32_t box[2] = {(cuuint32_t)cols, (cuuint32_t)rows}, ones[2] = {1, 1};
+    return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                  const_cast<void*>(base), dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 cudaError_t launch_scan(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream_t stream) {
     ScanParams p{};
