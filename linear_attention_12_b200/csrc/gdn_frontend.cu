@@ -313,149 +313,215 @@ __global__ void __launch_bounds__(32)
 //   dx[s] = sum_i w_i dy[s + 3 - i],   dw_i = sum_t dy[t] x[t - 3 + i].
 //
 // HBM-bound: raw rows and output gradients read once, raw gradients written once.
-// One warp walks a run of consecutive tokens of one head, each lane holding 4 channels:
-// a rolling window of three raw rows feeds the convolution, three partial rows of dx
-// wait for the tokens ahead of them, and dw runs in registers.  Runs overlap by the
-// three rows behind and ahead of them.
+// One warp walks a run of consecutive tokens of its channels: a rolling window of three raw
+// rows feeds the convolution, three partial rows of dx wait for the tokens ahead of them,
+// and dw runs in registers.  Runs overlap by the three rows behind and ahead of them.
 //
-// Every warp keeps FG_STAGES tiles of FG_ROWS rows (x and the output gradient) on their
-// way by TMA into its own part of shared memory, and takes four rows at a time: their
-// activations, and for q and k the two sums over the head, do not depend on one another, so
-// their latencies overlap.  The arithmetic goes two channels to an instruction (about 14 per
-// channel of v and 23 of q and k instead of 28 and 40).
-constexpr int FG_WARPS = 4;         // per block, each on its own
-constexpr int FG_BLOCKS = 4;        // blocks per SM, all runs at once
-constexpr int FG_STAGES = 3;
-constexpr int FG_STAGE_BYTES = 4096;  // of a warp: FG_ROWS rows of x, as many of the gradient
-template <typename IO>
-__host__ __device__ constexpr int fg_rows() { return FG_STAGE_BYTES / (2 * FD * (int)sizeof(IO)); }
-constexpr int FG_SMEM = FG_WARPS * FG_STAGES * (FG_STAGE_BYTES + 8) + 16;
+// Every warp keeps `stages` tiles of ROWS rows (x and the output gradient) on their way by TMA
+// into its own part of shared memory; within a tile nothing but the window joins the rows, so
+// their latencies overlap.  The arithmetic goes two channels to an instruction (about 16 per
+// channel of v and 23 of q and k; 28 and 40 without).
+//
+// What bounds it past the bytes is the latency that a warp's registers leave uncovered, so v
+// and q, k are kernels of their own: a warp of q or k holds a whole head (four channels a lane,
+// 168 registers, 12 warps an SM) for the sums over it; v needs no sums, and a warp holds half a
+// head (two channels a lane, 80 registers, 24 warps an SM).  One kernel for both, at 128
+// registers, took 597 us for 32,768 tokens of 16/48 bf16 heads.
+template <bool L2>
+struct FG {
+    static constexpr int P = L2 ? 2 : 1;           // pairs of channels a lane
+    static constexpr int CH = 64 * P;              // channels of a warp
+    static constexpr int WARPS = 4;                // per block, each on its own
+    static constexpr int BLOCKS = L2 ? 3 : 6;      // blocks per SM: all runs at once
+    static constexpr int STAGES = 3;
+    static constexpr int HALF = 8 * CH * 2;        // bytes of a stage's rows of x
+    static constexpr int RING = STAGES * 2 * HALF;  // bytes of a warp's ring
+    static constexpr int SMEM = WARPS * (RING + STAGES * 8) + 16;
+    template <typename IO>
+    static constexpr int rows() { return HALF / (CH * (int)sizeof(IO)); }
+};
 
 struct FrontendGradParams {
     FrontendGradArgs a;
     float* part;  // [runs, (2 H_qk + H_v) d, 4] partial sums of dw
-    int runs, run_len, blocks;  // blocks of the convolution part; the rest take the gates
+    int runs, run_len;
 };
 struct FrontendGradMaps {
-    CUtensorMap x[3], dout[3];
+    CUtensorMap x[2], dout[2];  // q and k, or v
 };
 
-// Four channels as two pairs.
-struct F4 {
-    float2 lo, hi;
+// A lane's channels.
+template <int P>
+struct Chans {
+    float2 c[P];
 };
-__device__ __forceinline__ F4 zero4() { return F4{both(0.f), both(0.f)}; }
-__device__ __forceinline__ F4 fma4(const F4& a, const F4& b, const F4& c) {
-    return F4{fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)};
+template <int P>
+__device__ __forceinline__ Chans<P> zeros() {
+    Chans<P> r;
+#pragma unroll
+    for (int i = 0; i < P; ++i) r.c[i] = both(0.f);
+    return r;
 }
-__device__ __forceinline__ F4 mul4(const F4& a, const F4& b) {
-    return F4{mul2(a.lo, b.lo), mul2(a.hi, b.hi)};
+template <int P>
+__device__ __forceinline__ Chans<P> fma_c(const Chans<P>& a, const Chans<P>& b, const Chans<P>& c) {
+    Chans<P> r;
+#pragma unroll
+    for (int i = 0; i < P; ++i) r.c[i] = fma2(a.c[i], b.c[i], c.c[i]);
+    return r;
 }
-__device__ __forceinline__ float dot4(const F4& a, const F4& b) {
-    const float2 s = fma2(a.hi, b.hi, mul2(a.lo, b.lo));
+template <int P>
+__device__ __forceinline__ Chans<P> mul_c(const Chans<P>& a, const Chans<P>& b) {
+    Chans<P> r;
+#pragma unroll
+    for (int i = 0; i < P; ++i) r.c[i] = mul2(a.c[i], b.c[i]);
+    return r;
+}
+template <int P>
+__device__ __forceinline__ float dot_c(const Chans<P>& a, const Chans<P>& b) {
+    float2 s = mul2(a.c[0], b.c[0]);
+#pragma unroll
+    for (int i = 1; i < P; ++i) s = fma2(a.c[i], b.c[i], s);
     return s.x + s.y;
 }
-template <typename IO>
-__device__ __forceinline__ F4 load4(const IO* p) {
-    const float4 v = Vec4<IO>::load(p);
-    return F4{make_float2(v.x, v.y), make_float2(v.z, v.w)};
+template <int P>
+__device__ __forceinline__ Chans<P> load_c(const __nv_bfloat16* p) {
+    uint32_t u[P];
+    if constexpr (P == 2) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        u[0] = v.x, u[1] = v.y;
+    } else {
+        u[0] = *reinterpret_cast<const uint32_t*>(p);
+    }
+    Chans<P> r;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+        r.c[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+    return r;
 }
-template <typename IO>
-__device__ __forceinline__ void store4(IO* p, const F4& v) {
-    Vec4<IO>::store(p, make_float4(v.lo.x, v.lo.y, v.hi.x, v.hi.y));
+template <int P>
+__device__ __forceinline__ Chans<P> load_c(const float* p) {
+    Chans<P> r;
+    if constexpr (P == 2) {
+        const float4 v = *reinterpret_cast<const float4*>(p);
+        r.c[0] = make_float2(v.x, v.y), r.c[1] = make_float2(v.z, v.w);
+    } else {
+        r.c[0] = *reinterpret_cast<const float2*>(p);
+    }
+    return r;
+}
+template <int P>
+__device__ __forceinline__ void store_c(__nv_bfloat16* p, const Chans<P>& v) {
+    if constexpr (P == 2)
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(pack_bf16x2(v.c[0].x, v.c[0].y), pack_bf16x2(v.c[1].x, v.c[1].y));
+    else
+        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.c[0].x, v.c[0].y);
+}
+template <int P>
+__device__ __forceinline__ void store_c(float* p, const Chans<P>& v) {
+    if constexpr (P == 2)
+        *reinterpret_cast<float4*>(p) = make_float4(v.c[0].x, v.c[0].y, v.c[1].x, v.c[1].y);
+    else
+        *reinterpret_cast<float2*>(p) = v.c[0];
 }
 
 // What a warp carries from row to row.
+template <int P>
 struct GradState {
-    F4 w[4], dw[4];
-    F4 x1, x2, x3;  // raw rows t - 1, t - 2, t - 3 (zeros before the sequence)
-    F4 d1, d2, d3;  // dx of tokens t - 1, t - 2, t - 3 so far
-    int lo;         // the first token whose dx is pending or stored here
+    Chans<P> w[4], dw[4];
+    Chans<P> x1, x2, x3;  // raw rows t - 1, t - 2, t - 3 (zeros before the sequence)
+    Chans<P> d1, d2, d3;  // dx of tokens t - 1, t - 2, t - 3 so far
+    int lo;               // the first token whose dx is pending or stored here
 };
 
 // Rows t .. t + NR - 1 of one sequence: x and dout at xs, gs (rows `pitch` elements apart);
-// dx of tokens t - 3 .. t + NR - 4 is complete after it and stored.
-template <int NR, bool L2, bool SILU, bool DW, typename IO>
-__device__ __forceinline__ void grad_rows(GradState& s, int t, const IO* xs, const IO* gs,
+// dx of tokens t - 3 .. t + NR - 4 is complete after it and stored.  ALL: every one of them
+// belongs to the run.
+template <int NR, bool L2, bool SILU, bool DW, bool ALL, typename IO, int P>
+__device__ __forceinline__ void grad_rows(GradState<P>& s, int t, const IO* xs, const IO* gs,
                                           int64_t pitch, IO* dx, int64_t rs, float eps) {
-    F4 x[NR + 3], u[NR], slope[NR], dy[NR];
+    Chans<P> x[NR + 3], u[NR], slope[NR], dy[NR];
     x[0] = s.x3, x[1] = s.x2, x[2] = s.x1;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        x[i + 3] = load4(xs + i * pitch);
-        dy[i] = load4(gs + i * pitch);
+        x[i + 3] = load_c<P>(xs + i * pitch);
+        dy[i] = load_c<P>(gs + i * pitch);
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        const F4 y = fma4(s.w[0], x[i], fma4(s.w[1], x[i + 1],
-                                              fma4(s.w[2], x[i + 2], mul4(s.w[3], x[i + 3]))));
+        const Chans<P> y = fma_c(
+            s.w[0], x[i],
+            fma_c(s.w[1], x[i + 1], fma_c(s.w[2], x[i + 2], mul_c(s.w[3], x[i + 3]))));
         u[i] = y;
         if (SILU) {
-            const F4 g{sigmoid2(y.lo), sigmoid2(y.hi)};
-            u[i] = mul4(y, g);
-            slope[i] = F4{fma2(u[i].lo, fma2(g.lo, both(-1.f), both(1.f)), g.lo),
-                          fma2(u[i].hi, fma2(g.hi, both(-1.f), both(1.f)), g.hi)};
+#pragma unroll
+            for (int c = 0; c < P; ++c) {
+                const float2 g = sigmoid2(y.c[c]);
+                u[i].c[c] = mul2(y.c[c], g);
+                slope[i].c[c] = fma2(u[i].c[c], fma2(g, both(-1.f), both(1.f)), g);
+            }
         }
     }
     if (L2) {
-        float ss[NR], ud[NR];
+        float2 su[NR];  // <u, u> and <u, dout>
 #pragma unroll
-        for (int i = 0; i < NR; ++i) ss[i] = dot4(u[i], u[i]), ud[i] = dot4(u[i], dy[i]);
+        for (int i = 0; i < NR; ++i) su[i] = make_float2(dot_c(u[i], u[i]), dot_c(u[i], dy[i]));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                ss[i] += __shfl_xor_sync(0xffffffffu, ss[i], o);
-                ud[i] += __shfl_xor_sync(0xffffffffu, ud[i], o);
-            }
+            for (int i = 0; i < NR; ++i)
+                su[i] = add2(su[i], make_float2(__shfl_xor_sync(0xffffffffu, su[i].x, o),
+                                                __shfl_xor_sync(0xffffffffu, su[i].y, o)));
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            const float r = rsqrtf(ss[i] + eps);
-            const float2 r2 = both(r), c = both(-r * r * r * ud[i]);
-            dy[i] = F4{fma2(u[i].lo, c, mul2(r2, dy[i].lo)), fma2(u[i].hi, c, mul2(r2, dy[i].hi))};
+            const float r = rsqrtf(su[i].x + eps);
+            const float2 r2 = both(r), k = both(-r * r * r * su[i].y);
+#pragma unroll
+            for (int c = 0; c < P; ++c) dy[i].c[c] = fma2(u[i].c[c], k, mul2(r2, dy[i].c[c]));
         }
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        if (SILU) dy[i] = mul4(dy[i], slope[i]);
+        if (SILU) dy[i] = mul_c(dy[i], slope[i]);
         if (DW)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s.dw[k] = fma4(dy[i], x[i + k], s.dw[k]);
-        const F4 done = fma4(s.w[0], dy[i], s.d3);
-        if (t + i - 3 >= s.lo) store4(dx + (t + i - 3) * rs, done);
-        s.d3 = fma4(s.w[1], dy[i], s.d2);
-        s.d2 = fma4(s.w[2], dy[i], s.d1);
-        s.d1 = mul4(s.w[3], dy[i]);
+            for (int k = 0; k < 4; ++k) s.dw[k] = fma_c(dy[i], x[i + k], s.dw[k]);
+        const Chans<P> done = fma_c(s.w[0], dy[i], s.d3);
+        if (ALL || t + i - 3 >= s.lo) store_c(dx + (t + i - 3) * rs, done);
+        s.d3 = fma_c(s.w[1], dy[i], s.d2);
+        s.d2 = fma_c(s.w[2], dy[i], s.d1);
+        s.d1 = mul_c(s.w[3], dy[i]);
     }
     s.x3 = x[NR], s.x2 = x[NR + 1], s.x1 = x[NR + 2];
 }
 
 // Nothing follows token t - 1 in its sequence or run: what waits is complete.
-template <typename IO>
-__device__ __forceinline__ void grad_flush(const GradState& s, int t, int tb, IO* dx, int64_t rs) {
-    if (t - 3 >= s.lo && t - 3 < tb) store4(dx + (t - 3) * rs, s.d3);
-    if (t - 2 >= s.lo && t - 2 < tb) store4(dx + (t - 2) * rs, s.d2);
-    if (t - 1 >= s.lo && t - 1 < tb) store4(dx + (t - 1) * rs, s.d1);
+template <typename IO, int P>
+__device__ __forceinline__ void grad_flush(const GradState<P>& s, int t, int tb, IO* dx, int64_t rs) {
+    if (t - 3 >= s.lo && t - 3 < tb) store_c(dx + (t - 3) * rs, s.d3);
+    if (t - 2 >= s.lo && t - 2 < tb) store_c(dx + (t - 2) * rs, s.d2);
+    if (t - 1 >= s.lo && t - 1 < tb) store_c(dx + (t - 1) * rs, s.d1);
 }
 
 template <typename IO, bool SILU, bool L2>
-__device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState& s, const IO* x,
-                                         const IO* go, IO* dx, int64_t rs, int ta, int tb,
-                                         int T_end, const CUtensorMap* mx, const CUtensorMap* mg,
-                                         int c0, uint8_t* ring, uint64_t* full,
-                                         volatile int* abort_flag) {
-    constexpr int ROWS = fg_rows<IO>();
+__device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<FG<L2>::P>& s,
+                                         const IO* x, const IO* go, IO* dx, int64_t rs, int ta,
+                                         int tb, int T_end, const CUtensorMap* mx,
+                                         const CUtensorMap* mg, int c0, uint8_t* ring,
+                                         uint64_t* full, volatile int* abort_flag) {
+    using F = FG<L2>;
+    constexpr int P = F::P, ROWS = F::template rows<IO>(), STAGES = F::STAGES;
     const int lane = threadIdx.x & 31;
     const int tiles = (tb - ta + ROWS - 1) / ROWS;
     const auto fetch = [&](int i) {
         if (i >= tiles || lane != 0) return;
-        uint8_t* d = ring + i % FG_STAGES * FG_STAGE_BYTES;
-        uint64_t* bar = &full[i % FG_STAGES];
-        mbar_arrive_expect_tx(bar, FG_STAGE_BYTES);
+        uint8_t* d = ring + i % STAGES * (2 * F::HALF);
+        uint64_t* bar = &full[i % STAGES];
+        mbar_arrive_expect_tx(bar, 2 * F::HALF);
         tma_load_2d(d, mx, c0, ta + i * ROWS, bar);
-        tma_load_2d(d + FG_STAGE_BYTES / 2, mg, c0, ta + i * ROWS, bar);
+        tma_load_2d(d + F::HALF, mg, c0, ta + i * ROWS, bar);
     };
-    for (int i = 0; i < FG_STAGES; ++i) fetch(i);
+    for (int i = 0; i < STAGES; ++i) fetch(i);
 
     // the sequence of token ta, and where the next one starts
     int n = 0, first = 0, next = T_end;
@@ -468,14 +534,14 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState& s
         first = max(a.cu_seqlens[n], 0);
         next = a.cu_seqlens[n + 1];
     }
-    s.x1 = ta - 1 >= first ? load4(x + (ta - 1) * rs) : zero4();
-    s.x2 = ta - 2 >= first ? load4(x + (ta - 2) * rs) : zero4();
-    s.x3 = ta - 3 >= first ? load4(x + (ta - 3) * rs) : zero4();
-    s.d1 = s.d2 = s.d3 = zero4();
+    s.x1 = ta - 1 >= first ? load_c<P>(x + (ta - 1) * rs) : zeros<P>();
+    s.x2 = ta - 2 >= first ? load_c<P>(x + (ta - 2) * rs) : zeros<P>();
+    s.x3 = ta - 3 >= first ? load_c<P>(x + (ta - 3) * rs) : zeros<P>();
+    s.d1 = s.d2 = s.d3 = zeros<P>();
     s.lo = max(first, ta);
     const auto start = [&](int t) {  // a sequence starts at token t
         grad_flush(s, t, tb, dx, rs);
-        s.x1 = s.x2 = s.x3 = s.d1 = s.d2 = s.d3 = zero4();
+        s.x1 = s.x2 = s.x3 = s.d1 = s.d2 = s.d3 = zeros<P>();
         s.lo = t;
         do {
             ++n;
@@ -484,123 +550,128 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState& s
     };
 
     for (int i = 0; i < tiles; ++i) {
-        if (!mbar_wait(&full[i % FG_STAGES], (i / FG_STAGES) & 1, abort_flag)) {
+        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, abort_flag)) {
             // the copies may still land: wait for them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
-            for (int k = i; k < min(i + FG_STAGES, tiles); ++k)
-                while (!mbar_try_wait(smem_u32(&full[k % FG_STAGES]), (k / FG_STAGES) & 1) &&
+            for (int k = i; k < min(i + STAGES, tiles); ++k)
+                while (!mbar_try_wait(smem_u32(&full[k % STAGES]), (k / STAGES) & 1) &&
                        globaltimer() - ts < kWaitLimitNs) {
                 }
             return;
         }
-        const IO* xs = reinterpret_cast<const IO*>(ring + i % FG_STAGES * FG_STAGE_BYTES) + 4 * lane;
-        const IO* gs = xs + ROWS * FD;
+        const IO* xs =
+            reinterpret_cast<const IO*>(ring + i % STAGES * (2 * F::HALF)) + 2 * P * lane;
+        const IO* gs = xs + ROWS * F::CH;
+        const int t0 = ta + i * ROWS;
+        if (t0 - 3 >= s.lo && t0 + ROWS <= tb && next >= t0 + ROWS) {
+            // a whole tile within the run and the sequence, as almost all are
+            constexpr int NR = 2;
+#pragma unroll
+            for (int r = 0; r < ROWS; r += NR)
+                grad_rows<NR, L2, SILU, true, true>(s, t0 + r, xs + r * F::CH, gs + r * F::CH, F::CH,
+                                                    dx, rs, a.eps);
+        } else {
 #pragma unroll 1
-        for (int r = 0; r < ROWS; r += 2) {
-            const int t = ta + i * ROWS + r;
-            if (t >= tb) break;
-            if (t == next) start(t);
-            if (t + 2 <= tb && next >= t + 2) {
-                grad_rows<2, L2, SILU, true>(s, t, xs + r * FD, gs + r * FD, FD, dx, rs, a.eps);
-            } else {
-#pragma unroll 1
-                for (int k = 0; k < 2 && t + k < tb; ++k) {
-                    if (t + k == next) start(t + k);
-                    grad_rows<1, L2, SILU, true>(s, t + k, xs + (r + k) * FD, gs + (r + k) * FD, FD,
-                                                 dx, rs, a.eps);
-                }
+            for (int r = 0; r < ROWS && t0 + r < tb; ++r) {
+                if (t0 + r == next) start(t0 + r);
+                grad_rows<1, L2, SILU, true, false>(s, t0 + r, xs + r * F::CH, gs + r * F::CH, F::CH,
+                                                    dx, rs, a.eps);
             }
         }
         __syncwarp();  // everyone has read the tile
-        fetch(i + FG_STAGES);
+        fetch(i + STAGES);
     }
     // the tokens ahead of the run's last three, for their dx alone
     const int te = min(tb + 3, T_end);
     int t = tb;
 #pragma unroll 1
     for (; t < te && t != next; ++t)
-        grad_rows<1, L2, SILU, false>(s, t, x + t * rs, go + t * rs, rs, dx, rs, a.eps);
+        grad_rows<1, L2, SILU, false, false>(s, t, x + t * rs, go + t * rs, rs, dx, rs, a.eps);
     grad_flush(s, t, tb, dx, rs);
 }
 
-template <typename IO, int ACT>
-__global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
+// L2: the heads of q and k; else v's, and the gates.
+template <typename IO, int ACT, bool L2>
+__global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
     frontend_grad_kernel(const __grid_constant__ FrontendGradMaps maps, const FrontendGradParams p) {
+    using F = FG<L2>;
+    constexpr int P = F::P;
     const FrontendGradArgs& a = p.a;
     const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
-    if ((int)blockIdx.x >= p.blocks) {  // the gates, element by element
-        const int64_t n = (int64_t)T_end * a.H_v;
-        const int64_t step = (int64_t)(gridDim.x - p.blocks) * (FG_WARPS * 32);
-        for (int64_t i = (int64_t)(blockIdx.x - p.blocks) * (FG_WARPS * 32) + threadIdx.x; i < n;
-             i += step) {
+    extern __shared__ __align__(128) uint8_t fg_sm[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t* ring = fg_sm + warp * F::RING;
+    uint64_t* full = reinterpret_cast<uint64_t*>(fg_sm + F::WARPS * F::RING) + warp * F::STAGES;
+    volatile int* abort_flag =
+        reinterpret_cast<volatile int*>(fg_sm + F::WARPS * (F::RING + F::STAGES * 8));
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (lane == 0) {
+        for (int i = 0; i < F::STAGES; ++i) mbar_init(&full[i], 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    if (!L2) {  // the gates, element by element, a share for every block
+        const int64_t n = (int64_t)T_end * a.H_v, all = (int64_t)gridDim.x * (F::WARPS * 32);
+        for (int64_t i = (int64_t)blockIdx.x * (F::WARPS * 32) + threadIdx.x; i < n; i += all) {
             const float be = sigmoidf(a.b[i]);
             a.da[i] = -sigmoidf(a.a[i]) * a.dlog_alpha[i];
             a.db[i] = be * (1.f - be) * a.dbeta[i];
         }
-        return;
     }
-    extern __shared__ __align__(128) uint8_t fg_sm[];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* ring = fg_sm + warp * FG_STAGES * FG_STAGE_BYTES;
-    uint64_t* full =
-        reinterpret_cast<uint64_t*>(fg_sm + FG_WARPS * FG_STAGES * FG_STAGE_BYTES) + warp * FG_STAGES;
-    volatile int* abort_flag =
-        reinterpret_cast<volatile int*>(fg_sm + FG_WARPS * FG_STAGES * (FG_STAGE_BYTES + 8));
-    if (threadIdx.x == 0) *abort_flag = 0;
-    if (lane == 0) {
-        for (int i = 0; i < FG_STAGES; ++i) mbar_init(&full[i], 1);
-        fence_mbar_init();
-    }
-    __syncthreads();
-    const int heads = 2 * a.H_qk + a.H_v;
-    const int64_t unit = (int64_t)blockIdx.x * FG_WARPS + warp;
-    if (unit >= (int64_t)p.runs * heads) return;
-    const int run = (int)(unit / heads), hid = (int)(unit - (int64_t)run * heads);
-    const int kind = hid < a.H_qk ? 0 : (hid < 2 * a.H_qk ? 1 : 2);
-    const int head = hid - (kind == 0 ? 0 : (kind == 1 ? a.H_qk : 2 * a.H_qk));
-    const int64_t rs = (int64_t)(kind == 2 ? a.H_v : a.H_qk) * FD;
-    const int64_t off = (int64_t)head * FD + 4 * lane;
-    const IO* x = static_cast<const IO*>(kind == 0 ? a.x[0] : (kind == 1 ? a.x[1] : a.x[2])) + off;
+    // unit: a run of a group of F::CH channels
+    const int groups = L2 ? 2 * a.H_qk : 2 * a.H_v;
+    const int64_t unit = (int64_t)blockIdx.x * F::WARPS + warp;
+    if (unit >= (int64_t)p.runs * groups) return;
+    const int run = (int)(unit / groups), g = (int)(unit - (int64_t)run * groups);
+    const int which = L2 && g >= a.H_qk ? 1 : 0;  // k
+    const int c0 = (g - (which ? a.H_qk : 0)) * F::CH;  // the group's first channel of its tensor
+    const int64_t rs = (int64_t)(L2 ? a.H_qk : a.H_v) * FD;
+    const int64_t off = c0 + 2 * P * lane;
+    const int t3 = L2 ? which : 2;
+    const IO* x = static_cast<const IO*>(t3 == 0 ? a.x[0] : (t3 == 1 ? a.x[1] : a.x[2])) + off;
     const IO* go =
-        static_cast<const IO*>(kind == 0 ? a.dout[0] : (kind == 1 ? a.dout[1] : a.dout[2])) + off;
-    IO* dx = static_cast<IO*>(kind == 0 ? a.dx[0] : (kind == 1 ? a.dx[1] : a.dx[2])) + off;
+        static_cast<const IO*>(t3 == 0 ? a.dout[0] : (t3 == 1 ? a.dout[1] : a.dout[2])) + off;
+    IO* dx = static_cast<IO*>(t3 == 0 ? a.dx[0] : (t3 == 1 ? a.dx[1] : a.dx[2])) + off;
+    const int64_t wc = (int64_t)t3 * a.H_qk * FD + off;  // the lane's channel of the weight
 
-    GradState s;
-    {
-        // 4 channels x 4 taps, channel-major -> the taps' pairs of channels
-        const float4* wp = reinterpret_cast<const float4*>(a.w + ((int64_t)hid * FD + 4 * lane) * 4);
-        const float4 c0 = wp[0], c1 = wp[1], c2 = wp[2], c3 = wp[3];
-        s.w[0] = F4{make_float2(c0.x, c1.x), make_float2(c2.x, c3.x)};
-        s.w[1] = F4{make_float2(c0.y, c1.y), make_float2(c2.y, c3.y)};
-        s.w[2] = F4{make_float2(c0.z, c1.z), make_float2(c2.z, c3.z)};
-        s.w[3] = F4{make_float2(c0.w, c1.w), make_float2(c2.w, c3.w)};
-        for (int k = 0; k < 4; ++k) s.dw[k] = zero4();
+    GradState<P> s;
+    // the lane's channels x 4 taps, channel-major -> the taps' pairs of channels
+    const float4* wp = reinterpret_cast<const float4*>(a.w) + wc;
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+        const float4 u = wp[2 * c], v = wp[2 * c + 1];
+        s.w[0].c[c] = make_float2(u.x, v.x);
+        s.w[1].c[c] = make_float2(u.y, v.y);
+        s.w[2].c[c] = make_float2(u.z, v.z);
+        s.w[3].c[c] = make_float2(u.w, v.w);
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s.dw[k] = zeros<P>();
     const int64_t first = (int64_t)run * p.run_len;
     const int ta = (int)min(first, (int64_t)T_end), tb = (int)min(first + p.run_len, (int64_t)T_end);
-    if (ta < tb) {
-        if (kind == 2)
-            grad_run<IO, ACT == GDN_ACT_SILU, false>(a, s, x, go, dx, rs, ta, tb, T_end, &maps.x[2],
-                                                     &maps.dout[2], head * FD, ring, full, abort_flag);
-        else
-            grad_run<IO, ACT == GDN_ACT_SILU, true>(
-                a, s, x, go, dx, rs, ta, tb, T_end, kind == 0 ? &maps.x[0] : &maps.x[1],
-                kind == 0 ? &maps.dout[0] : &maps.dout[1], head * FD, ring, full, abort_flag);
+    if (ta < tb)
+        grad_run<IO, ACT == GDN_ACT_SILU, L2>(a, s, x, go, dx, rs, ta, tb, T_end,
+                                              which ? &maps.x[1] : &maps.x[0],
+                                              which ? &maps.dout[1] : &maps.dout[0], c0, ring, full,
+                                              abort_flag);
+    float4* o = reinterpret_cast<float4*>(p.part) + (int64_t)run * (2 * a.H_qk + a.H_v) * FD + wc;
+#pragma unroll
+    for (int c = 0; c < P; ++c) {
+        o[2 * c] = make_float4(s.dw[0].c[c].x, s.dw[1].c[c].x, s.dw[2].c[c].x, s.dw[3].c[c].x);
+        o[2 * c + 1] = make_float4(s.dw[0].c[c].y, s.dw[1].c[c].y, s.dw[2].c[c].y, s.dw[3].c[c].y);
     }
-    float4* o = reinterpret_cast<float4*>(p.part) + ((int64_t)run * heads + hid) * FD + 4 * lane;
-    o[0] = make_float4(s.dw[0].lo.x, s.dw[1].lo.x, s.dw[2].lo.x, s.dw[3].lo.x);
-    o[1] = make_float4(s.dw[0].lo.y, s.dw[1].lo.y, s.dw[2].lo.y, s.dw[3].lo.y);
-    o[2] = make_float4(s.dw[0].hi.x, s.dw[1].hi.x, s.dw[2].hi.x, s.dw[3].hi.x);
-    o[3] = make_float4(s.dw[0].hi.y, s.dw[1].hi.y, s.dw[2].hi.y, s.dw[3].hi.y);
 }
 
-// Runs per head: all warps at once, runs of at least 32 tokens, whole tiles of rows.
+// Runs per channel: all warps of either kernel at once (v has the most), runs of at least 32
+// tokens, whole tiles of rows.
 struct GradRuns {
     int runs, len;
 };
-GradRuns frontend_grad_runs(int T, int heads) {
-    const long long warps = (long long)device_sms() * FG_BLOCKS * FG_WARPS;
-    long long runs = warps / heads;
+GradRuns frontend_grad_runs(int T, int H_qk, int H_v) {
+    const long long sms = device_sms();
+    long long runs = sms * FG<true>::BLOCKS * FG<true>::WARPS / (2 * H_qk);
+    const long long rv = sms * FG<false>::BLOCKS * FG<false>::WARPS / (2 * H_v);
+    if (runs > rv) runs = rv;
     const long long most = ((long long)T + 31) / 32;
     if (runs > most) runs = most;
     if (runs < 1) runs = 1;
@@ -609,55 +680,62 @@ GradRuns frontend_grad_runs(int T, int heads) {
     return GradRuns{(int)((T + len - 1) / len), (int)len};
 }
 
-template <typename IO, int ACT>
-cudaError_t launch_frontend_grad(const FrontendGradParams& p, unsigned grid, cudaStream_t stream) {
+template <typename IO, int ACT, bool L2>
+cudaError_t launch_frontend_grad(const FrontendGradParams& p, cudaStream_t stream) {
+    using F = FG<L2>;
     const FrontendGradArgs& a = p.a;
     FrontendGradMaps maps{};
-    for (int k = 0; k < 3; ++k) {
-        const int64_t C = (int64_t)(k == 2 ? a.H_v : a.H_qk) * FD;
-        if (!tile_map(&maps.x[k], a.x[k], a.bf16, a.T, C, C, FD, fg_rows<IO>()) ||
-            !tile_map(&maps.dout[k], a.dout[k], a.bf16, a.T, C, C, FD, fg_rows<IO>()))
+    const int64_t C = (int64_t)(L2 ? a.H_qk : a.H_v) * FD;
+    for (int k = 0; k < (L2 ? 2 : 1); ++k) {
+        const int t3 = L2 ? k : 2;
+        constexpr int rows = F::template rows<IO>();
+        if (!tile_map(&maps.x[k], a.x[t3], a.bf16, a.T, C, C, F::CH, rows) ||
+            !tile_map(&maps.dout[k], a.dout[t3], a.bf16, a.T, C, C, F::CH, rows))
             return cudaErrorInvalidValue;
     }
-    const auto kernel = frontend_grad_kernel<IO, ACT>;
+    const auto kernel = frontend_grad_kernel<IO, ACT, L2>;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FG_SMEM);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, FG_WARPS * 32, FG_SMEM, stream>>>(maps, p);
+    const long long groups = L2 ? 2ll * a.H_qk : 2ll * a.H_v;
+    const long long blocks = (p.runs * groups + F::WARPS - 1) / F::WARPS;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    kernel<<<(unsigned)blocks, F::WARPS * 32, F::SMEM, stream>>>(maps, p);
     return cudaGetLastError();
+}
+
+template <typename IO, int ACT>
+cudaError_t launch_frontend_grads(const FrontendGradParams& p, cudaStream_t stream) {
+    const cudaError_t e = launch_frontend_grad<IO, ACT, true>(p, stream);
+    return e != cudaSuccess ? e : launch_frontend_grad<IO, ACT, false>(p, stream);
 }
 
 }  // namespace
 
 size_t frontend_backward_workspace_bytes(int T, int H_qk, int H_v) {
     const int heads = 2 * H_qk + H_v;
-    return T == 0 ? 0 : (size_t)frontend_grad_runs(T, heads).runs * heads * FD * 4 * sizeof(float);
+    return T == 0 ? 0
+                  : (size_t)frontend_grad_runs(T, H_qk, H_v).runs * heads * FD * 4 * sizeof(float);
 }
 
 cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
                                      cudaStream_t stream) {
-    const int heads = 2 * a.H_qk + a.H_v;
     FrontendGradParams p{};
     p.a = a;
     p.part = static_cast<float*>(workspace);
     if (a.T > 0) {
-        const GradRuns g = frontend_grad_runs(a.T, heads);
+        const GradRuns g = frontend_grad_runs(a.T, a.H_qk, a.H_v);
         p.runs = g.runs;
         p.run_len = g.len;
-        const long long blocks = ((long long)p.runs * heads + FG_WARPS - 1) / FG_WARPS;
-        const long long gates = ((long long)a.T * a.H_v + 1023) / 1024;  // 8 or more per thread
-        const long long gate_blocks = gates < 148 ? gates : 148;
-        if (blocks + gate_blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-        p.blocks = (int)blocks;
-        const unsigned grid = (unsigned)(blocks + gate_blocks);
         const cudaError_t e =
-            a.bf16 ? (a.silu ? launch_frontend_grad<__nv_bfloat16, GDN_ACT_SILU>(p, grid, stream)
-                             : launch_frontend_grad<__nv_bfloat16, GDN_ACT_NONE>(p, grid, stream))
-                   : (a.silu ? launch_frontend_grad<float, GDN_ACT_SILU>(p, grid, stream)
-                             : launch_frontend_grad<float, GDN_ACT_NONE>(p, grid, stream));
+            a.bf16 ? (a.silu ? launch_frontend_grads<__nv_bfloat16, GDN_ACT_SILU>(p, stream)
+                             : launch_frontend_grads<__nv_bfloat16, GDN_ACT_NONE>(p, stream))
+                   : (a.silu ? launch_frontend_grads<float, GDN_ACT_SILU>(p, stream)
+                             : launch_frontend_grads<float, GDN_ACT_NONE>(p, stream));
         if (e != cudaSuccess) return e;
     }
-    return launch_column_sums(p.part, nullptr, a.dw, nullptr, p.runs, heads * FD * 4, stream);
+    return launch_column_sums(p.part, nullptr, a.dw, nullptr, p.runs,
+                              (2 * a.H_qk + a.H_v) * FD * 4, stream);
 }
 
 cudaError_t launch_frontend(const void* q_raw, const void* k_raw, const void* v_raw,
