@@ -24,6 +24,7 @@
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_sums.cuh"
 
 namespace gdn {
 
@@ -329,11 +330,11 @@ __global__ void __launch_bounds__(32)
 // registers, took 597 us for 32,768 tokens of 16/48 bf16 heads.
 template <bool L2>
 struct FG {
-    static constexpr int P = L2 ? 2 : 1;           // pairs of channels a lane
-    static constexpr int CH = 64 * P;              // channels of a warp
+    static constexpr int P = 2;                    // pairs of channels a lane
+    static constexpr int CH = 64 * P;              // channels of a warp: a head
     static constexpr int WARPS = 4;                // per block, each on its own
-    static constexpr int BLOCKS = L2 ? 3 : 6;      // blocks per SM: all runs at once
-    static constexpr int STAGES = 3;
+    static constexpr int BLOCKS = 3;      // blocks per SM: all runs at once
+    static constexpr int STAGES = 2;               // (a power of two)
     static constexpr int HALF = 8 * CH * 2;        // bytes of a stage's rows of x
     static constexpr int RING = STAGES * 2 * HALF;  // bytes of a warp's ring
     static constexpr int SMEM = WARPS * (RING + STAGES * 8) + 16;
@@ -343,7 +344,7 @@ struct FG {
 
 struct FrontendGradParams {
     FrontendGradArgs a;
-    float* part;  // [runs, (2 H_qk + H_v) d, 4] partial sums of dw
+    float* part;  // [runs, channels of the kernel, 4] partial sums of dw
     int runs, run_len;
 };
 struct FrontendGradMaps {
@@ -512,11 +513,12 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<FG
     using F = FG<L2>;
     constexpr int P = F::P, ROWS = F::template rows<IO>(), STAGES = F::STAGES;
     const int lane = threadIdx.x & 31;
-    const int tiles = (tb - ta + ROWS - 1) / ROWS;
+    // (the three tokens ahead of the run's last are read too, for the run's dx alone)
+    const int te = min(tb + 3, T_end), tiles = (te - ta + ROWS - 1) / ROWS;
     const auto fetch = [&](int i) {
         if (i >= tiles || lane != 0) return;
-        uint8_t* d = ring + i % STAGES * (2 * F::HALF);
-        uint64_t* bar = &full[i % STAGES];
+        uint8_t* d = ring + (i & (STAGES - 1)) * (2 * F::HALF);
+        uint64_t* bar = &full[(i & (STAGES - 1))];
         mbar_arrive_expect_tx(bar, 2 * F::HALF);
         tma_load_2d(d, mx, c0, ta + i * ROWS, bar);
         tma_load_2d(d + F::HALF, mg, c0, ta + i * ROWS, bar);
@@ -550,47 +552,54 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<FG
     };
 
     for (int i = 0; i < tiles; ++i) {
-        if (!mbar_wait(&full[i % STAGES], (i / STAGES) & 1, abort_flag)) {
+        if (!mbar_wait(&full[(i & (STAGES - 1))], (i / STAGES) & 1, abort_flag)) {
             // the copies may still land: wait for them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
             for (int k = i; k < min(i + STAGES, tiles); ++k)
-                while (!mbar_try_wait(smem_u32(&full[k % STAGES]), (k / STAGES) & 1) &&
+                while (!mbar_try_wait(smem_u32(&full[(k & (STAGES - 1))]), (k / STAGES) & 1) &&
                        globaltimer() - ts < kWaitLimitNs) {
                 }
             return;
         }
         const IO* xs =
-            reinterpret_cast<const IO*>(ring + i % STAGES * (2 * F::HALF)) + 2 * P * lane;
+            reinterpret_cast<const IO*>(ring + (i & (STAGES - 1)) * (2 * F::HALF)) + 2 * P * lane;
         const IO* gs = xs + ROWS * F::CH;
         const int t0 = ta + i * ROWS;
-        if (t0 - 3 >= s.lo && t0 + ROWS <= tb && next >= t0 + ROWS) {
+        if (t0 == next) start(t0);
+        if (t0 + ROWS <= tb && next >= t0 + ROWS) {
             // a whole tile within the run and the sequence, as almost all are
             constexpr int NR = 2;
+            if (t0 - 3 >= s.lo) {
 #pragma unroll
-            for (int r = 0; r < ROWS; r += NR)
-                grad_rows<NR, L2, SILU, true, true>(s, t0 + r, xs + r * F::CH, gs + r * F::CH, F::CH,
-                                                    dx, rs, a.eps);
+                for (int r = 0; r < ROWS; r += NR)
+                    grad_rows<NR, L2, SILU, true, true>(s, t0 + r, xs + r * F::CH, gs + r * F::CH,
+                                                        F::CH, dx, rs, a.eps);
+            } else {  // the first one
+#pragma unroll
+                for (int r = 0; r < ROWS; r += NR)
+                    grad_rows<NR, L2, SILU, true, false>(s, t0 + r, xs + r * F::CH, gs + r * F::CH,
+                                                         F::CH, dx, rs, a.eps);
+            }
         } else {
 #pragma unroll 1
-            for (int r = 0; r < ROWS && t0 + r < tb; ++r) {
-                if (t0 + r == next) start(t0 + r);
-                grad_rows<1, L2, SILU, true, false>(s, t0 + r, xs + r * F::CH, gs + r * F::CH, F::CH,
-                                                    dx, rs, a.eps);
+            for (int r = 0; r < ROWS && t0 + r < te; ++r) {
+                const int t = t0 + r;
+                if (t == next) start(t);
+                if (t < tb)
+                    grad_rows<1, L2, SILU, true, false>(s, t, xs + r * F::CH, gs + r * F::CH, F::CH,
+                                                        dx, rs, a.eps);
+                else if (s.lo < tb)
+                    grad_rows<1, L2, SILU, false, false>(s, t, xs + r * F::CH, gs + r * F::CH, F::CH,
+                                                         dx, rs, a.eps);
             }
         }
         __syncwarp();  // everyone has read the tile
         fetch(i + STAGES);
     }
-    // the tokens ahead of the run's last three, for their dx alone
-    const int te = min(tb + 3, T_end);
-    int t = tb;
-#pragma unroll 1
-    for (; t < te && t != next; ++t)
-        grad_rows<1, L2, SILU, false, false>(s, t, x + t * rs, go + t * rs, rs, dx, rs, a.eps);
-    grad_flush(s, t, tb, dx, rs);
+    grad_flush(s, te, tb, dx, rs);
 }
 
-// L2: the heads of q and k; else v's, and the gates.
+// L2: the heads of q and k; else v's.
 template <typename IO, int ACT, bool L2>
 __global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
     frontend_grad_kernel(const __grid_constant__ FrontendGradMaps maps, const FrontendGradParams p) {
@@ -610,16 +619,8 @@ __global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
         fence_mbar_init();
     }
     __syncthreads();
-    if (!L2) {  // the gates, element by element, a share for every block
-        const int64_t n = (int64_t)T_end * a.H_v, all = (int64_t)gridDim.x * (F::WARPS * 32);
-        for (int64_t i = (int64_t)blockIdx.x * (F::WARPS * 32) + threadIdx.x; i < n; i += all) {
-            const float be = sigmoidf(a.b[i]);
-            a.da[i] = -sigmoidf(a.a[i]) * a.dlog_alpha[i];
-            a.db[i] = be * (1.f - be) * a.dbeta[i];
-        }
-    }
     // unit: a run of a group of F::CH channels
-    const int groups = L2 ? 2 * a.H_qk : 2 * a.H_v;
+    const int groups = L2 ? 2 * a.H_qk : a.H_v;
     const int64_t unit = (int64_t)blockIdx.x * F::WARPS + warp;
     if (unit >= (int64_t)p.runs * groups) return;
     const int run = (int)(unit / groups), g = (int)(unit - (int64_t)run * groups);
@@ -632,7 +633,8 @@ __global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
     const IO* go =
         static_cast<const IO*>(t3 == 0 ? a.dout[0] : (t3 == 1 ? a.dout[1] : a.dout[2])) + off;
     IO* dx = static_cast<IO*>(t3 == 0 ? a.dx[0] : (t3 == 1 ? a.dx[1] : a.dx[2])) + off;
-    const int64_t wc = (int64_t)t3 * a.H_qk * FD + off;  // the lane's channel of the weight
+    // the lane's channel of the weight, and among the kernel's channels
+    const int64_t wc = (int64_t)t3 * a.H_qk * FD + off, pc = (int64_t)which * a.H_qk * FD + off;
 
     GradState<P> s;
     // the lane's channels x 4 taps, channel-major -> the taps' pairs of channels
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
                                               which ? &maps.x[1] : &maps.x[0],
                                               which ? &maps.dout[1] : &maps.dout[0], c0, ring, full,
                                               abort_flag);
-    float4* o = reinterpret_cast<float4*>(p.part) + (int64_t)run * (2 * a.H_qk + a.H_v) * FD + wc;
+    float4* o = reinterpret_cast<float4*>(p.part) + (int64_t)run * groups * F::CH + pc;
 #pragma unroll
     for (int c = 0; c < P; ++c) {
         o[2 * c] = make_float4(s.dw[0].c[c].x, s.dw[1].c[c].x, s.dw[2].c[c].x, s.dw[3].c[c].x);
@@ -662,16 +664,46 @@ __global__ void __launch_bounds__(FG<L2>::WARPS * 32, FG<L2>::BLOCKS)
     }
 }
 
-// Runs per channel: all warps of either kernel at once (v has the most), runs of at least 32
-// tokens, whole tiles of rows.
+// The last step: dw from the partial sums of q and k (blockIdx.y 0) and of v (1), and beside
+// them, since those wait for memory more than they use it, the gates (2; it took 45 us at the
+// start of v's blocks for 32,768 tokens of 48 heads, and almost nothing here).
+constexpr int FG_LAST = 256;
+__global__ void __launch_bounds__(FG_LAST)
+    frontend_grad_last_kernel(const FrontendGradArgs a, const ColumnSums qk, const ColumnSums v) {
+    if (blockIdx.y < 2) {
+        column_sums<FG_LAST / 32>(blockIdx.y ? v : qk, blockIdx.x);
+        return;
+    }
+    const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
+    const int64_t n = (int64_t)T_end * a.H_v, all = (int64_t)gridDim.x * FG_LAST;
+    for (int64_t i = (int64_t)blockIdx.x * FG_LAST + threadIdx.x; i < n; i += 4 * all) {
+        float va[4], vb[4], ga[4], gb[4];  // (all loads before the first store)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t j = i + k * all < n ? i + k * all : i;
+            va[k] = a.a[j], vb[k] = a.b[j], ga[k] = a.dlog_alpha[j], gb[k] = a.dbeta[j];
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t j = i + k * all;
+            const float be = sigmoidf(vb[k]);
+            if (j < n) {
+                a.da[j] = -sigmoidf(va[k]) * ga[k];
+                a.db[j] = be * (1.f - be) * gb[k];
+            }
+        }
+    }
+}
+
+// Runs per channel: all warps of the kernel at once, runs of at least 32 tokens, whole tiles
+// of rows.
 struct GradRuns {
     int runs, len;
 };
-GradRuns frontend_grad_runs(int T, int H_qk, int H_v) {
-    const long long sms = device_sms();
-    long long runs = sms * FG<true>::BLOCKS * FG<true>::WARPS / (2 * H_qk);
-    const long long rv = sms * FG<false>::BLOCKS * FG<false>::WARPS / (2 * H_v);
-    if (runs > rv) runs = rv;
+template <bool L2>
+GradRuns frontend_grad_runs(int T, int heads) {
+    const long long warps = (long long)device_sms() * FG<L2>::BLOCKS * FG<L2>::WARPS;
+    long long runs = warps / heads;
     const long long most = ((long long)T + 31) / 32;
     if (runs > most) runs = most;
     if (runs < 1) runs = 1;
@@ -679,13 +711,21 @@ GradRuns frontend_grad_runs(int T, int H_qk, int H_v) {
     len = (len + 7) / 8 * 8;
     return GradRuns{(int)((T + len - 1) / len), (int)len};
 }
+// Bytes of the partial sums of q and k (v's lie behind them), or of v.
+template <bool L2>
+size_t frontend_grad_part(int T, int heads) {
+    return (size_t)frontend_grad_runs<L2>(T, heads).runs * heads * FD * 4 * sizeof(float);
+}
 
 template <typename IO, int ACT, bool L2>
-cudaError_t launch_frontend_grad(const FrontendGradParams& p, cudaStream_t stream) {
+cudaError_t launch_frontend_grad(const FrontendGradArgs& a, float* part, cudaStream_t stream) {
     using F = FG<L2>;
-    const FrontendGradArgs& a = p.a;
+    const int H = L2 ? a.H_qk : a.H_v;
+    const int heads = L2 ? 2 * H : H;
+    const GradRuns g = frontend_grad_runs<L2>(a.T, heads);
+    const FrontendGradParams p{a, part, g.runs, g.len};
     FrontendGradMaps maps{};
-    const int64_t C = (int64_t)(L2 ? a.H_qk : a.H_v) * FD;
+    const int64_t C = (int64_t)H * FD;
     for (int k = 0; k < (L2 ? 2 : 1); ++k) {
         const int t3 = L2 ? k : 2;
         constexpr int rows = F::template rows<IO>();
@@ -697,45 +737,47 @@ cudaError_t launch_frontend_grad(const FrontendGradParams& p, cudaStream_t strea
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, F::SMEM);
     if (e != cudaSuccess) return e;
-    const long long groups = L2 ? 2ll * a.H_qk : 2ll * a.H_v;
-    const long long blocks = (p.runs * groups + F::WARPS - 1) / F::WARPS;
+    const long long blocks = ((long long)p.runs * heads + F::WARPS - 1) / F::WARPS;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     kernel<<<(unsigned)blocks, F::WARPS * 32, F::SMEM, stream>>>(maps, p);
     return cudaGetLastError();
 }
 
 template <typename IO, int ACT>
-cudaError_t launch_frontend_grads(const FrontendGradParams& p, cudaStream_t stream) {
-    const cudaError_t e = launch_frontend_grad<IO, ACT, true>(p, stream);
-    return e != cudaSuccess ? e : launch_frontend_grad<IO, ACT, false>(p, stream);
+cudaError_t launch_frontend_grads(const FrontendGradArgs& a, float* part_qk, float* part_v,
+                                  cudaStream_t stream) {
+    const cudaError_t e = launch_frontend_grad<IO, ACT, true>(a, part_qk, stream);
+    return e != cudaSuccess ? e : launch_frontend_grad<IO, ACT, false>(a, part_v, stream);
 }
 
 }  // namespace
 
 size_t frontend_backward_workspace_bytes(int T, int H_qk, int H_v) {
-    const int heads = 2 * H_qk + H_v;
-    return T == 0 ? 0
-                  : (size_t)frontend_grad_runs(T, H_qk, H_v).runs * heads * FD * 4 * sizeof(float);
+    return T == 0 ? 0 : frontend_grad_part<true>(T, 2 * H_qk) + frontend_grad_part<false>(T, H_v);
 }
 
 cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
                                      cudaStream_t stream) {
-    FrontendGradParams p{};
-    p.a = a;
-    p.part = static_cast<float*>(workspace);
+    float *qk = nullptr, *v = nullptr;
+    int runs_qk = 0, runs_v = 0;
     if (a.T > 0) {
-        const GradRuns g = frontend_grad_runs(a.T, a.H_qk, a.H_v);
-        p.runs = g.runs;
-        p.run_len = g.len;
+        qk = static_cast<float*>(workspace);
+        v = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                     frontend_grad_part<true>(a.T, 2 * a.H_qk));
+        runs_qk = frontend_grad_runs<true>(a.T, 2 * a.H_qk).runs;
+        runs_v = frontend_grad_runs<false>(a.T, a.H_v).runs;
         const cudaError_t e =
-            a.bf16 ? (a.silu ? launch_frontend_grads<__nv_bfloat16, GDN_ACT_SILU>(p, stream)
-                             : launch_frontend_grads<__nv_bfloat16, GDN_ACT_NONE>(p, stream))
-                   : (a.silu ? launch_frontend_grads<float, GDN_ACT_SILU>(p, stream)
-                             : launch_frontend_grads<float, GDN_ACT_NONE>(p, stream));
+            a.bf16 ? (a.silu ? launch_frontend_grads<__nv_bfloat16, GDN_ACT_SILU>(a, qk, v, stream)
+                             : launch_frontend_grads<__nv_bfloat16, GDN_ACT_NONE>(a, qk, v, stream))
+                   : (a.silu ? launch_frontend_grads<float, GDN_ACT_SILU>(a, qk, v, stream)
+                             : launch_frontend_grads<float, GDN_ACT_NONE>(a, qk, v, stream));
         if (e != cudaSuccess) return e;
     }
-    return launch_column_sums(p.part, nullptr, a.dw, nullptr, p.runs,
-                              (2 * a.H_qk + a.H_v) * FD * 4, stream);
+    const int cq = 2 * a.H_qk * FD * 4, cv = a.H_v * FD * 4;
+    const int blocks = ((cq > cv ? cq : cv) + 31) / 32;
+    frontend_grad_last_kernel<<<dim3(blocks, a.T > 0 ? 3 : 2), FG_LAST, 0, stream>>>(
+        a, ColumnSums{qk, a.dw, runs_qk, cq}, ColumnSums{v, a.dw + cq, runs_v, cv});
+    return cudaGetLastError();
 }
 
 cudaError_t launch_frontend(const void* q_raw, const void* k_raw, const void* v_raw,

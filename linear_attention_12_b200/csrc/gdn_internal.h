@@ -125,10 +125,6 @@ size_t group_norm_backward_workspace_bytes(int T, int H, int d, int weight_heads
 cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, float* dbias,
                                        void* workspace, cudaStream_t stream);
 
-// out0 = column sums of part0 [rows, cols] in a fixed order, and out1 of part1 unless null.
-cudaError_t launch_column_sums(const float* part0, const float* part1, float* out0, float* out1,
-                               int rows, int cols, cudaStream_t stream);
-
 // Gradients of the front end.
 struct FrontendGradArgs {
     const void* x[3];     // q_raw, k_raw, v_raw

@@ -20,6 +20,7 @@
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
 #include "gdn_internal.h"
+#include "gdn_sums.cuh"
 
 namespace gdn {
 
@@ -367,27 +368,10 @@ __global__ void __launch_bounds__(NT, NV == 1 ? bwd_blocks(PLAIN, WIDE && sizeof
     }
 }
 
-// Column sums of part [rows, cols] into out (blockIdx.y: the first pair, then the
-// second), in an order that does not depend on timing.  Bound by the latency of its
-// loads: 32 rows at once per block, eight of them in flight per thread.
-__global__ void __launch_bounds__(1024)
-    column_sums_kernel(const float* part0, const float* part1, float* out0, float* out1, int rows,
-                       int cols) {
-    __shared__ float sm[32][33];
-    const float* part = blockIdx.y ? part1 : part0;
-    float* out = blockIdx.y ? out1 : out0;
-    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + tx;
-    float s = 0.f;
-    if (c < cols)
-#pragma unroll 8
-        for (int r = ty; r < rows; r += 32) s += part[(int64_t)r * cols + c];
-    sm[ty][tx] = s;
-    __syncthreads();
-    s = sm[tx][ty];  // warp ty adds column ty
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (tx == 0 && blockIdx.x * 32 + ty < cols) out[blockIdx.x * 32 + ty] = s;
+// Column sums of up to two matrices (blockIdx.y).
+template <int RT>
+__global__ void __launch_bounds__(32 * RT) column_sums_kernel(const ColumnSums a, const ColumnSums b) {
+    column_sums<RT>(blockIdx.y ? b : a, blockIdx.x);
 }
 
 // Lanes of a group: a power of two that its vectors fill, 4 to 32.
@@ -503,13 +487,6 @@ int partial_rows(int T, int H, int d, bool per_head, bool wide, bool bf16, bool 
 
 }  // namespace
 
-cudaError_t launch_column_sums(const float* part0, const float* part1, float* out0, float* out1,
-                               int rows, int cols, cudaStream_t stream) {
-    column_sums_kernel<<<dim3((cols + 31) / 32, out1 ? 2 : 1), 1024, 0, stream>>>(
-        part0, part1, out0, out1, rows, cols);
-    return cudaGetLastError();
-}
-
 cudaError_t launch_group_norm(const GroupNormArgs& a, cudaStream_t stream) {
     if (a.T == 0) return cudaSuccess;
     return launch_any(params_of(a), a.bf16, false, stream);
@@ -544,7 +521,13 @@ cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, f
         if (e != cudaSuccess) return e;
         rows = partial_rows(a.T, a.H, a.d, per_head, wide_norm(p, a.bf16), a.bf16, is_plain(p));
     }
-    return launch_column_sums(p.dw_part, p.db_part, dweight, dbias, rows, cols, stream);
+    const ColumnSums sw{p.dw_part, dweight, rows, cols}, sb{p.db_part, dbias, rows, cols};
+    const dim3 grid((cols + 31) / 32, dbias ? 2 : 1);
+    if (rows > 64)
+        column_sums_kernel<32><<<grid, 1024, 0, stream>>>(sw, sb);
+    else
+        column_sums_kernel<8><<<grid, 256, 0, stream>>>(sw, sb);
+    return cudaGetLastError();
 }
 
 }  // namespace gdn

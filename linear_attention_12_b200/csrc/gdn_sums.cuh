@@ -1,0 +1,44 @@
+// gdn_sums.cuh -- the second step of a gradient that is a sum over tokens: kernels leave one
+// row of partial sums per run of tokens, and these are added in an order that does not depend
+// on timing.
+#pragma once
+
+#include <stdint.h>
+
+namespace gdn {
+
+// out = column sums of part [rows, cols].
+struct ColumnSums {
+    const float* part;
+    float* out;
+    int rows, cols;
+};
+
+// Columns 32 bx .. of a, by a block of 32 x RT threads.  Bound by the latency of its loads:
+// RT rows at once, eight loads in flight per thread.
+template <int RT>
+__device__ __forceinline__ void column_sums(const ColumnSums& a, int bx) {
+    __shared__ float sm[RT][33];
+    const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+    const int c = bx * 32 + tx;
+    float s = 0.f;
+    if (c < a.cols)
+        for (int r = ty; r < a.rows; r += 8 * RT) {
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = r + k * RT < a.rows ? a.part[(int64_t)(r + k * RT) * a.cols + c] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s += v[k];
+        }
+    sm[ty][tx] = s;
+    __syncthreads();
+    if (ty == 0 && c < a.cols) {
+        s = 0.f;
+#pragma unroll
+        for (int q = 0; q < RT; ++q) s += sm[q][tx];
+        a.out[c] = s;
+    }
+}
+
+}  // namespace gdn
