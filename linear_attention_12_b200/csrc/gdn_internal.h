@@ -20,6 +20,9 @@ cudaError_t launch_decode_multi(const void* q, const void* k, const void* v,
 // also stages bf16 copies of q, k, v).
 size_t prefill_workspace_bytes(int N, int T, int H_qk, int H_v, bool bf16, int P);
 
+// Devices (by index) whose properties are remembered between calls.
+constexpr int kKnownDevices = 64;
+
 // SM count of the current device (148 when there is none).
 int device_sms();
 

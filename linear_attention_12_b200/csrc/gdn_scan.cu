@@ -56,7 +56,6 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 // infinity or a NaN cannot cross.
 constexpr int CW = 64;             // channels of a tile
 constexpr int MAX_CLUSTER = 16;    // (above 8 only where the device grants it)
-constexpr int MAX_DEVICES = 16;    // whose cluster room is remembered
 constexpr int SCAN_BAR = 1;        // named barrier of the consumer warps
 
 struct ScanParams {
@@ -570,11 +569,20 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
             (BWD && !tile_map(&mh, p.h, sizeof(IO) == 2, p.T, p.C, p.hs, CW, SM::TT)))
             return cudaErrorInvalidValue;
     }
-    cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
+    // the kernel's attributes and how many clusters of R blocks a device holds: asked once
+    static std::atomic<int> ready[kKnownDevices];
+    static std::atomic<int> room[kKnownDevices][MAX_CLUSTER + 1];  // 0: not asked yet
+    const bool known = dev < kKnownDevices;
+    if (!known || !ready[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (known) ready[dev].store(1, std::memory_order_release);
+    }
     cudaLaunchConfig_t cfg{};
     cfg.blockDim = dim3((WARPS + 1) * 32);
     cfg.dynamicSmemBytes = SM::BYTES;
@@ -588,12 +596,9 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     // much as the first), and no more than there are tiles.
     const long long groups = ((long long)p.C + CW - 1) / CW;
     const long long tiles = ((long long)p.T + SM::TT - 1) / SM::TT;
-    static std::atomic<int> room[MAX_DEVICES][MAX_CLUSTER + 1];  // 0: not asked yet
-    int dev = 0;
-    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return e;
     int R = (int)(tiles < MAX_CLUSTER ? (tiles < 1 ? 1 : tiles) : MAX_CLUSTER);
     for (; R > 1; --R) {
-        int fit = dev < MAX_DEVICES ? room[dev][R].load(std::memory_order_relaxed) : 0;
+        int fit = known ? room[dev][R].load(std::memory_order_relaxed) : 0;
         if (fit == 0) {
             cfg.gridDim = dim3(R);
             attr[0].val.clusterDim.x = R;
@@ -601,7 +606,7 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
                 cudaGetLastError();
                 fit = -1;
             }
-            if (dev < MAX_DEVICES) room[dev][R].store(fit, std::memory_order_relaxed);
+            if (known) room[dev][R].store(fit, std::memory_order_relaxed);
         }
         if (groups <= fit) break;
     }

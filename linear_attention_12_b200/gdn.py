@@ -116,6 +116,8 @@ class GDNError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load ``libgdn.so`` (once).  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -460,9 +462,7 @@ def _dtype_of(t, name):
     return got
 
 
-def _rows(t, name, dtype, shape, device) -> int:
-    """Row stride of a token-major tensor whose rows are dense (a column slice of a wider
-    tensor will do); raises where it is not of this dtype, shape and device."""
+def _expect(t, name, dtype, shape, device):
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -471,11 +471,20 @@ def _rows(t, name, dtype, shape, device) -> int:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    cols = 1
+
+
+def _rows(t, name, dtype, shape, device, cols) -> int:
+    """Row stride of a token-major tensor whose rows of ``cols`` elements are dense (a column
+    slice of a wider tensor will do); raises where it is not of this dtype, shape, device."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == shape and t.is_contiguous()):
+        return cols
+    _expect(t, name, dtype, shape, device)
+    dense = 1
     for i in range(len(shape) - 1, 0, -1):
-        if shape[i] != 1 and t.stride(i) != cols:
+        if shape[i] != 1 and t.stride(i) != dense:
             raise ValueError(f"the rows of {name} must be dense, got strides {t.stride()}")
-        cols *= shape[i]
+        dense *= shape[i]
     if shape[0] <= 1:
         return cols
     if t.stride(0) < cols:
@@ -484,16 +493,16 @@ def _rows(t, name, dtype, shape, device) -> int:
 
 
 def _dense(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+            and t.shape == shape and t.is_contiguous()):
+        return
+    _expect(t, name, dtype, shape, device)
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _new(t):
+    """A dense tensor of t's shape, dtype and device."""
+    return torch.empty_like(t, memory_format=torch.contiguous_format, requires_grad=False)
 
 
 def _at(t):
@@ -511,7 +520,7 @@ def _placed(fn):
             raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
         device = first.device
         if stream is None:
-            if device.index == torch.cuda.current_device():
+            if device.index == torch._C._cuda_getDevice():
                 return fn(first, *args, **kw)
             with torch.cuda.device(device):
                 return fn(first, *args, **kw)
@@ -534,8 +543,9 @@ def _placed(fn):
 
 
 def _here(device):
-    """The current stream of a device, as a cudaStream_t."""
-    return torch.cuda.current_stream(device).cuda_stream
+    """The current stream of a device, as a cudaStream_t (what
+    ``torch.cuda.current_stream(device).cuda_stream`` says, without the objects)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _workspace(workspace, need, device):
@@ -551,15 +561,17 @@ def _nbytes(t):
 
 def _scan_sizes(first, cu_seqlens, device):
     """(T, C, the shape of a token's channels, N, pointer of cu_seqlens)."""
-    if first.dim() < 2:
-        raise ValueError(f"expected [T, ...channels], got {tuple(first.shape)}")
-    T, chans = first.shape[0], first.shape[1:]
+    shape = first.shape
+    if len(shape) < 2:
+        raise ValueError(f"expected [T, ...channels], got {tuple(shape)}")
+    chans = shape[1:]
+    C = chans[0] if len(chans) == 1 else chans.numel()
     if cu_seqlens is None:
-        return T, chans.numel(), chans, 1, None
+        return shape[0], C, chans, 1, None
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
     _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
-    return T, chans.numel(), chans, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
+    return shape[0], C, chans, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
 
 
 @_placed
@@ -575,14 +587,14 @@ def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_s
     other calls."""
     io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
     T, C, chans, N, cu = _scan_sizes(x, cu_seqlens, dev)
-    xs = _rows(x, "x", x.dtype, shape, dev)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
+    xs = _rows(x, "x", x.dtype, shape, dev, C)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
     if h0 is not None:
         _dense(h0, "h0", torch.float32, (N, *chans), dev)
     if h is None:
-        h, hs = torch.empty(shape, dtype=x.dtype, device=dev), C
+        h, hs = _new(x), C
     else:
-        hs = _rows(h, "h", x.dtype, shape, dev)
+        hs = _rows(h, "h", x.dtype, shape, dev, C)
     if h_final is not None:
         _dense(h_final, "h_final", torch.float32, (N, *chans), dev)
     elif want_state:
@@ -604,19 +616,19 @@ def scan_backward(log_alpha, h, dh, h0=None, dh_final=None, cu_seqlens=None, *, 
     fp32 (None if not wanted)."""
     io, gate, dev, shape = _dtype_of(h, "h"), _dtype_of(log_alpha, "log_alpha"), h.device, h.shape
     T, C, chans, N, cu = _scan_sizes(h, cu_seqlens, dev)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
-    hs, dhs = _rows(h, "h", h.dtype, shape, dev), _rows(dh, "dh", h.dtype, shape, dev)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
+    hs, dhs = _rows(h, "h", h.dtype, shape, dev, C), _rows(dh, "dh", h.dtype, shape, dev, C)
     for t, name in ((h0, "h0"), (dh_final, "dh_final")):
         if t is not None:
             _dense(t, name, torch.float32, (N, *chans), dev)
     if dx is None:
-        dx, dxs = torch.empty(shape, dtype=h.dtype, device=dev), C
+        dx, dxs = _new(h), C
     else:
-        dxs = _rows(dx, "dx", h.dtype, shape, dev)
+        dxs = _rows(dx, "dx", h.dtype, shape, dev, C)
     if dlog_alpha is None:
-        dlog_alpha, dlas = torch.empty(shape, dtype=log_alpha.dtype, device=dev), C
+        dlog_alpha, dlas = _new(log_alpha), C
     else:
-        dlas = _rows(dlog_alpha, "dlog_alpha", log_alpha.dtype, shape, dev)
+        dlas = _rows(dlog_alpha, "dlog_alpha", log_alpha.dtype, shape, dev, C)
     dh0 = torch.empty((N, *chans), dtype=torch.float32, device=dev) if want_dh0 else None
     st = lib().gdn_scan_backward(log_alpha.data_ptr(), las, h.data_ptr(), hs, dh.data_ptr(), dhs,
                                  _at(h0), _at(dh_final), cu, N, T, C, io, gate, dx.data_ptr(), dxs,
@@ -632,13 +644,13 @@ def scan_step(x, log_alpha, state, *, h=None):
     place to ``exp(log_alpha) state + x``.  Returns ``h``, the new state in x's type."""
     io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
     B, C, _, _, _ = _scan_sizes(x, None, dev)
-    xs = _rows(x, "x", x.dtype, shape, dev)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev)
+    xs = _rows(x, "x", x.dtype, shape, dev, C)
+    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
     _dense(state, "state", torch.float32, shape, dev)
     if h is None:
-        h, hs = torch.empty(shape, dtype=x.dtype, device=dev), C
+        h, hs = _new(x), C
     else:
-        hs = _rows(h, "h", x.dtype, shape, dev)
+        hs = _rows(h, "h", x.dtype, shape, dev, C)
     st = lib().gdn_scan_step(x.data_ptr(), xs, log_alpha.data_ptr(), las, state.data_ptr(), B, C,
                              io, gate, h.data_ptr(), hs, _here(dev))
     if st != GDN_OK:
@@ -658,8 +670,9 @@ def _norm_args(x, weight, bias, z):
     _dense(weight, "weight", torch.float32, weight.shape, dev)
     if bias is not None:
         _dense(bias, "bias", torch.float32, weight.shape, dev)
-    return (T, H, d, 1 if weight.dim() == 1 else H, io, _rows(x, "x", x.dtype, x.shape, dev),
-            0 if z is None else _rows(z, "z", x.dtype, x.shape, dev))
+    C = H * d
+    return (T, H, d, C, 1 if weight.dim() == 1 else H, io, _rows(x, "x", x.dtype, x.shape, dev, C),
+            0 if z is None else _rows(z, "z", x.dtype, x.shape, dev, C))
 
 
 @_placed
@@ -670,10 +683,11 @@ def group_norm(x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6
     or "mean" (centred).  ``weight`` and ``bias``: fp32 [d] or [H, d].  x, z and y may be
     column slices of wider tensors.  Returns ``y`` in x's type.  ``stream``: as for the
     other calls."""
-    T, H, d, wh, io, xs, zs = _norm_args(x, weight, bias, z)
+    T, H, d, C, wh, io, xs, zs = _norm_args(x, weight, bias, z)
     if y is None:
-        y = torch.empty((T, H, d), dtype=x.dtype, device=x.device)
-    ys = _rows(y, "y", x.dtype, x.shape, x.device)
+        y, ys = _new(x), C
+    else:
+        ys = _rows(y, "y", x.dtype, x.shape, x.device, C)
     st = lib().gdn_group_norm(x.data_ptr(), xs, _at(z), zs, weight.data_ptr(), _at(bias), T, H, d,
                               wh, _choice(norm, _NORMS, "norm"), _choice(act, _ACTS, "act"), eps,
                               io, y.data_ptr(), ys, _here(x.device))
@@ -690,21 +704,24 @@ def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="si
     Returns ``(dx, dweight, dbias, dz)``: dx and dz in x's type, dweight and dbias fp32 of
     weight's shape; dbias None without a bias, dz None without a gate.  ``dx`` and ``dz``
     may be given (column slices of wider tensors will do)."""
-    T, H, d, wh, io, xs, zs = _norm_args(x, weight, bias, z)
+    T, H, d, C, wh, io, xs, zs = _norm_args(x, weight, bias, z)
     dev = x.device
-    dys = _rows(dy, "dy", x.dtype, x.shape, dev)
+    dys = _rows(dy, "dy", x.dtype, x.shape, dev, C)
     if dx is None:
-        dx = torch.empty((T, H, d), dtype=x.dtype, device=dev)
-    dxs = _rows(dx, "dx", x.dtype, x.shape, dev)
+        dx, dxs = _new(x), C
+    else:
+        dxs = _rows(dx, "dx", x.dtype, x.shape, dev, C)
     if z is None and dz is not None:
         raise ValueError("dz without z")
     dzs = 0
     if z is not None:
         if dz is None:
-            dz = torch.empty((T, H, d), dtype=x.dtype, device=dev)
-        dzs = _rows(dz, "dz", x.dtype, x.shape, dev)
-    dw = torch.empty_like(weight, requires_grad=False)
-    db = None if bias is None else torch.empty_like(weight, requires_grad=False)
+            dz = _new(x)
+            dzs = C
+        else:
+            dzs = _rows(dz, "dz", x.dtype, x.shape, dev, C)
+    dw = _new(weight)
+    db = None if bias is None else _new(weight)
     L = lib()
     if workspace is None:
         need = L.gdn_group_norm_backward_workspace_size(T, H, d, wh, io)
@@ -731,21 +748,27 @@ def frontend_backward(q_raw, k_raw, v_raw, conv_w, a, b, dq, dk, dv, dlog_alpha,
     type, the others fp32.  Rows from ``cu_seqlens[-1]`` on stay unwritten."""
     if q_raw.dim() != 3 or v_raw.dim() != 3:
         raise ValueError("q_raw, k_raw and v_raw must be [T, H, d]")
-    io, dt, dev = _dtype_of(q_raw, "q_raw"), q_raw.dtype, q_raw.device
-    T, H_qk, dk_ = q_raw.shape
-    H_v, dv_ = v_raw.shape[1:]
-    for t, name in ((q_raw, "q_raw"), (k_raw, "k_raw"), (dq, "dq"), (dk, "dk")):
-        _dense(t, name, dt, q_raw.shape, dev)
-    for t, name in ((v_raw, "v_raw"), (dv, "dv")):
-        _dense(t, name, dt, (T, H_v, dv_), dev)
-    for t, name in ((a, "a"), (b, "b"), (dlog_alpha, "dlog_alpha"), (dbeta, "dbeta")):
-        _dense(t, name, torch.float32, (T, H_v), dev)
-    _dense(conv_w, "conv_w", torch.float32, ((2 * H_qk + H_v) * dk_, 4), dev)
+    io, dt, dev, qs, vs = (_dtype_of(q_raw, "q_raw"), q_raw.dtype, q_raw.device, q_raw.shape,
+                           v_raw.shape)
+    T, H_qk, dk_ = qs
+    _, H_v, dv_ = vs
+    if vs[0] != T:
+        raise ValueError(f"v_raw has {vs[0]} tokens, q_raw {T}")
+    gs, f32 = (T, H_v), torch.float32
+    _dense(q_raw, "q_raw", dt, qs, dev)
+    _dense(k_raw, "k_raw", dt, qs, dev)
+    _dense(v_raw, "v_raw", dt, vs, dev)
+    _dense(dq, "dq", dt, qs, dev)
+    _dense(dk, "dk", dt, qs, dev)
+    _dense(dv, "dv", dt, vs, dev)
+    _dense(a, "a", f32, gs, dev)
+    _dense(b, "b", f32, gs, dev)
+    _dense(dlog_alpha, "dlog_alpha", f32, gs, dev)
+    _dense(dbeta, "dbeta", f32, gs, dev)
+    _dense(conv_w, "conv_w", f32, ((2 * H_qk + H_v) * dk_, 4), dev)
     _, _, _, N, cu = _scan_sizes(q_raw, cu_seqlens, dev)
-    dq_raw, dk_raw, dv_raw = (torch.empty(t.shape, dtype=dt, device=dev)
-                              for t in (q_raw, k_raw, v_raw))
-    dw = torch.empty(conv_w.shape, dtype=torch.float32, device=dev)
-    da, db = (torch.empty((T, H_v), dtype=torch.float32, device=dev) for _ in range(2))
+    dq_raw, dk_raw, dv_raw, dw, da, db = (_new(q_raw), _new(k_raw), _new(v_raw), _new(conv_w),
+                                          _new(a), _new(b))
     L = lib()
     if workspace is None:
         workspace = _workspace(None, L.gdn_frontend_backward_workspace_size(T, H_qk, H_v, dk_, dv_,
