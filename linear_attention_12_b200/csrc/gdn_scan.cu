@@ -542,15 +542,47 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     cluster_sync();  // nobody ends while others may still send to it
 }
 
-template <typename IO, typename G>
-__global__ void __launch_bounds__(256) scan_step_kernel(const ScanArgs p) {
-    const int64_t n = (int64_t)p.T * p.C;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
-        const int64_t b = i / p.C, c = i - b * p.C;
-        const float a = expf(to_f(static_cast<const G*>(p.la)[b * p.la_stride + c]));
-        const float h = fmaf(a, p.h_final[i], to_f(static_cast<const IO*>(p.x)[b * p.x_stride + c]));
-        p.h_final[i] = h;
-        static_cast<IO*>(p.h)[b * p.h_stride + c] = from_f<IO>(h);
+// ---- one token of each of B sequences ----
+//
+// Bound by bytes at large B and by the launch at small: one pass, V channels a thread
+// (4 where rows are aligned: 16-byte accesses to the state; 256 x 6144 bf16 took 14.3 us with
+// one channel a thread).
+constexpr int STEP_THREADS = 128;
+
+template <typename T, int V>
+__device__ __forceinline__ void load_chans(const T* p, float2 (&v)[(V + 1) / 2]) {
+    if constexpr (V == 4 && sizeof(T) == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(p);
+        v[0] = Pair<__nv_bfloat16>::widen(u.x), v[1] = Pair<__nv_bfloat16>::widen(u.y);
+    } else if constexpr (V == 4) {
+        const float4 u = *reinterpret_cast<const float4*>(p);
+        v[0] = make_float2(u.x, u.y), v[1] = make_float2(u.z, u.w);
+    } else {
+        v[0] = make_float2(to_f(p[0]), 0.f);
+    }
+}
+
+template <typename IO, typename G, int V>
+__global__ void __launch_bounds__(STEP_THREADS) scan_step_kernel(const ScanArgs p, const int cblocks) {
+    constexpr int NP = (V + 1) / 2;
+    const int64_t b = blockIdx.x / cblocks;
+    const int c = ((int)(blockIdx.x - b * cblocks) * STEP_THREADS + threadIdx.x) * V;
+    if (c >= p.C) return;
+    float* state = p.h_final + b * p.C + c;
+    IO* h = static_cast<IO*>(p.h) + b * p.h_stride + c;
+    float2 l[NP], x[NP], s[NP];
+    load_chans<float, V>(state, s);
+    load_chans<G, V>(static_cast<const G*>(p.la) + b * p.la_stride + c, l);
+    load_chans<IO, V>(static_cast<const IO*>(p.x) + b * p.x_stride + c, x);
+#pragma unroll
+    for (int i = 0; i < NP; ++i) s[i] = fma2(exp2ch(l[i]), s[i], x[i]);
+    if constexpr (V == 4) {
+        *reinterpret_cast<float4*>(state) = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+        put_two(h, s[0]);
+        put_two(h + 2, s[1]);
+    } else {
+        state[0] = s[0].x;
+        h[0] = from_f<IO>(s[0].x);
     }
 }
 
@@ -695,17 +727,28 @@ cudaError_t launch_scan_backward(const ScanGradArgs& a, bool bf16, bool gate_bf1
     return launch_direction<true>(p, bf16, gate_bf16, stream);
 }
 
-cudaError_t launch_scan_step(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream_t stream) {
-    const int64_t blocks = ((int64_t)a.T * a.C + 255) / 256;
-    const int grid = (int)(blocks < 148 * 64 ? blocks : 148 * 64);
-    if (bf16) {
-        if (gate_bf16) scan_step_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-        else scan_step_kernel<__nv_bfloat16, float><<<grid, 256, 0, stream>>>(a);
-    } else {
-        if (gate_bf16) scan_step_kernel<float, __nv_bfloat16><<<grid, 256, 0, stream>>>(a);
-        else scan_step_kernel<float, float><<<grid, 256, 0, stream>>>(a);
-    }
+template <typename IO, typename G>
+static cudaError_t launch_step(const ScanArgs& a, cudaStream_t stream) {
+    const bool wide = a.C % 4 == 0 && reinterpret_cast<uintptr_t>(a.h_final) % 16 == 0 &&
+                      wide_rows(a.x, a.x_stride, sizeof(IO)) &&
+                      wide_rows(a.la, a.la_stride, sizeof(G)) &&
+                      wide_rows(a.h, a.h_stride, sizeof(IO));
+    const int per = STEP_THREADS * (wide ? 4 : 1), cblocks = (a.C + per - 1) / per;
+    const long long blocks = (long long)a.T * cblocks;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (wide)
+        scan_step_kernel<IO, G, 4><<<(unsigned)blocks, STEP_THREADS, 0, stream>>>(a, cblocks);
+    else
+        scan_step_kernel<IO, G, 1><<<(unsigned)blocks, STEP_THREADS, 0, stream>>>(a, cblocks);
     return cudaGetLastError();
+}
+
+cudaError_t launch_scan_step(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream_t stream) {
+    if (bf16)
+        return gate_bf16 ? launch_step<__nv_bfloat16, __nv_bfloat16>(a, stream)
+                         : launch_step<__nv_bfloat16, float>(a, stream);
+    return gate_bf16 ? launch_step<float, __nv_bfloat16>(a, stream)
+                     : launch_step<float, float>(a, stream);
 }
 
 }  // namespace gdn
