@@ -55,7 +55,8 @@ def _scale(x, dy, w, b, z, norm, eps):
 
 
 SIZES = [(1, 1, 1), (1, 1, 128), (3, 2, 8), (5, 3, 17), (7, 48, 128), (130, 5, 80), (33, 1, 1024),
-         (9, 3, 1000), (2, 2, 1023), (64, 7, 96), (4099, 2, 16), (601, 33, 64), (2, 700, 4)]
+         (9, 3, 1000), (2, 2, 1023), (64, 7, 96), (4099, 2, 16), (601, 33, 64), (2, 700, 4), (40, 3, 18), (21, 5, 130), (12, 2, 258),
+         (6, 3, 1022), (9, 2, 190)]
 
 
 @pytest.mark.parametrize("T,H,d", SIZES)
@@ -102,10 +103,10 @@ def test_large_sums_are_accurate():
 
 
 @pytest.mark.parametrize("io", [BF16, F32])
-@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("shift", [0, 1, 2])
 def test_column_slices(io, shift):
-    """Inputs and outputs that are column slices of wider tensors, on the wide path (shift 0)
-    and off its alignment (shift 1); what lies beside them stays as it was."""
+    """Inputs and outputs that are column slices of wider tensors, on the wide path (shift 0),
+    aligned to pairs of bf16 (2) and off both (1); what lies beside them stays as it was."""
     T, H, d = 37, 3, 64
     x, dy, w, b, z = _case(T, H, d, io, 9)
     n = H * d
