@@ -324,9 +324,9 @@ __global__ void __launch_bounds__(32)
 // head, for the sums over a head of q or k and because rows of 256 bytes keep the memory busy
 // (with rows of 128 bytes v's part took 246 us instead of 210 us even with its arithmetic left
 // out).  12 warps an SM at 168 registers: with 128 registers and 16 warps the spills cost more
-// than the warps bring (32,768 tokens of 16/48 bf16 heads: 597 us against 546 us).
-constexpr int FG_WARPS = 4;                     // per block, each on its own
-constexpr int FG_BLOCKS = 3;                    // blocks per SM: all runs at once
+// than the warps bring (32,768 tokens of 16/48 bf16 heads: 428 us against 395 us).
+constexpr int FG_WARPS = 1;                     // per block: each on its own, and its slot free at its end
+constexpr int FG_BLOCKS = 12;                   // blocks per SM: all runs at once
 constexpr int FG_STAGES = 2;                    // (a power of two)
 constexpr int FG_HALF = 8 * FD * 2;             // bytes of a stage's rows of x: 8 of bf16, 4 of fp32
 constexpr int FG_RING = FG_STAGES * 2 * FG_HALF;  // bytes of a warp's ring
@@ -562,7 +562,7 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
         if (t0 == next) start(t0);
         if (t0 + ROWS <= tb && next >= t0 + ROWS) {
             // a whole tile within the run and the sequence, as almost all are
-            constexpr int NR = 2;
+            constexpr int NR = 4;
             if (t0 - 3 >= s.lo) {
 #pragma unroll
                 for (int r = 0; r < ROWS; r += NR)
@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
     const FrontendGradArgs& a = p.a;
     const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
     extern __shared__ __align__(128) uint8_t fg_sm[];
+    allow_next_step();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t* ring = fg_sm + warp * FG_RING;
     uint64_t* full = reinterpret_cast<uint64_t*>(fg_sm + FG_WARPS * FG_RING) + warp * FG_STAGES;
@@ -663,14 +664,15 @@ __global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
     }
 }
 
-// The last step: dw from the partial sums of q and k (blockIdx.y 0) and of v (1), and beside
-// it, since that waits for memory more than it uses it, the gates (2; they took 45 us at the start of the blocks of v
-// for 32,768 tokens of 48 heads).
+// The last step: the gates (blockIdx.y 0), which need nothing of the first and fill the SMs as
+// its warps end (at the start of the blocks of v they took 45 us for 32,768 tokens of 48
+// heads), and dw from the partial sums of q and k (1) and of v (2).
 constexpr int FG_LAST = 256;
 __global__ void __launch_bounds__(FG_LAST)
     frontend_grad_last_kernel(const FrontendGradArgs a, const ColumnSums qk, const ColumnSums v) {
-    if (blockIdx.y < 2) {
-        column_sums<FG_LAST / 32>(blockIdx.y ? v : qk, blockIdx.x);
+    if (blockIdx.y > 0) {
+        wait_for_first_step();
+        column_sums<FG_LAST / 32>(blockIdx.y == 1 ? qk : v, blockIdx.x);
         return;
     }
     const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
@@ -760,9 +762,9 @@ cudaError_t launch_frontend_backward(const FrontendGradArgs& a, void* workspace,
         if (e != cudaSuccess) return e;
     }
     const int blocks = ((cq > cv ? cq : cv) + 31) / 32;
-    frontend_grad_last_kernel<<<dim3(blocks, a.T > 0 ? 3 : 2), FG_LAST, 0, stream>>>(
-        a, ColumnSums{p.qk.part, a.dw, p.qk.runs, cq}, ColumnSums{p.v.part, a.dw + cq, p.v.runs, cv});
-    return cudaGetLastError();
+    return launch_second_step(frontend_grad_last_kernel, dim3(blocks, 3), FG_LAST, stream, a,
+                              ColumnSums{p.qk.part, a.dw, p.qk.runs, cq},
+                              ColumnSums{p.v.part, a.dw + cq, p.v.runs, cv});
 }
 
 cudaError_t launch_frontend(const void* q_raw, const void* k_raw, const void* v_raw,

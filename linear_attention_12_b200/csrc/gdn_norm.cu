@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(NT, NV == 1 ? bwd_blocks(PLAIN, A == WIDE && s
     using V = Vec<IO, A, LG>;
     constexpr int GPB = NT / LG;
     extern __shared__ float part[];  // [GPB][d], for the sums over a block's groups
+    allow_next_step();
     const Place<LG> at(p);
     const int lane = at.lane, d = p.d;
     float2 w[NV][V::NP], b[NV][V::NP], dw[NV][V::NP], db[NV][V::NP];
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(NT, NV == 1 ? bwd_blocks(PLAIN, A == WIDE && s
 // Column sums of up to two matrices (blockIdx.y).
 template <int RT>
 __global__ void __launch_bounds__(32 * RT) column_sums_kernel(const ColumnSums a, const ColumnSums b) {
+    wait_for_first_step();
     column_sums<RT>(blockIdx.y ? b : a, blockIdx.x);
 }
 
@@ -551,11 +553,8 @@ cudaError_t launch_group_norm_backward(const GroupNormArgs& a, float* dweight, f
     }
     const ColumnSums sw{p.dw_part, dweight, rows, cols}, sb{p.db_part, dbias, rows, cols};
     const dim3 grid((cols + 31) / 32, dbias ? 2 : 1);
-    if (rows > 64)
-        column_sums_kernel<32><<<grid, 1024, 0, stream>>>(sw, sb);
-    else
-        column_sums_kernel<8><<<grid, 256, 0, stream>>>(sw, sb);
-    return cudaGetLastError();
+    return rows > 64 ? launch_second_step(column_sums_kernel<32>, grid, 1024, stream, sw, sb)
+                     : launch_second_step(column_sums_kernel<8>, grid, 256, stream, sw, sb);
 }
 
 }  // namespace gdn

@@ -3,9 +3,36 @@
 // on timing.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace gdn {
+
+// The second step's launch does not wait for the first one's end: its blocks come in as the
+// first one's leave, and those that read what the first wrote wait for its end themselves.
+// Every block of the first step allows that (once they all have, the second may start); the
+// last block of the second ends behind the first, so what follows in the stream is ordered
+// behind both.
+__device__ __forceinline__ void allow_next_step() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_first_step() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename... P, typename... A>
+cudaError_t launch_second_step(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream,
+                               const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 // out = column sums of part [rows, cols].
 struct ColumnSums {
