@@ -74,13 +74,11 @@ struct Pair;
 template <>
 struct Pair<float> {
     using Raw = float2;
-    static __device__ __forceinline__ Raw make(float a, float b) { return make_float2(a, b); }
     static __device__ __forceinline__ float2 widen(Raw v) { return v; }
 };
 template <>
 struct Pair<__nv_bfloat16> {
     using Raw = uint32_t;
-    static __device__ __forceinline__ Raw make(float a, float b) { return pack_bf16x2(a, b); }
     static __device__ __forceinline__ float2 widen(Raw u) {
         return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
@@ -92,29 +90,26 @@ struct Pair<__nv_bfloat16> {
 template <typename T, bool TILED>
 struct Tile {
     static constexpr int PITCH = CW * (int)sizeof(T) + (TILED ? 0 : 16);
-    static __device__ __forceinline__ uint32_t shift(const void* base, int64_t row, int64_t stride,
+    // Where in its first granule a row starts, and what that moves by from row to row.
+    static __device__ __forceinline__ uint32_t shift(const void* base, int row, int64_t stride,
                                                      int c0) {
         const uint32_t at = (uint32_t)reinterpret_cast<uintptr_t>(base);
         return (at + ((uint32_t)row * (uint32_t)stride + (uint32_t)c0) * (uint32_t)sizeof(T)) & 15u;
     }
+    static __device__ __forceinline__ uint32_t shift_step(int64_t stride) {
+        return (uint32_t)stride * (uint32_t)sizeof(T);
+    }
     static __device__ __forceinline__ typename Pair<T>::Raw at(const uint8_t* tile, int r, int lane,
-                                                               const void* base, int64_t row,
-                                                               int64_t stride, int c0) {
-        if (TILED)
+                                                               uint32_t shift) {
+        if constexpr (TILED) {
             return reinterpret_cast<const typename Pair<T>::Raw*>(tile + r * PITCH)[lane];
-        const T* p = reinterpret_cast<const T*>(tile + r * PITCH + shift(base, row, stride, c0));
-        return Pair<T>::make(to_f(p[lane]), to_f(p[lane + 32]));
-    }
-    // The granules of one row that hold its n channels from c0 on.
-    static __device__ __forceinline__ const uint8_t* granule(const void* base, int64_t row,
-                                                             int64_t stride, int c0) {
-        return reinterpret_cast<const uint8_t*>(
-            reinterpret_cast<uintptr_t>(static_cast<const T*>(base) + row * stride + c0) &
-            ~(uintptr_t)15);
-    }
-    static __device__ __forceinline__ uint32_t bytes(const void* base, int64_t row, int64_t stride,
-                                                     int c0, int n) {
-        return (shift(base, row, stride, c0) + n * (uint32_t)sizeof(T) + 15u) & ~15u;
+        } else if constexpr (sizeof(T) == 2) {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(tile + r * PITCH + shift) + lane;
+            return (uint32_t)p[0] | (uint32_t)p[32] << 16;
+        } else {
+            const float* p = reinterpret_cast<const float*>(tile + r * PITCH + shift) + lane;
+            return make_float2(p[0], p[32]);
+        }
     }
 };
 __device__ __forceinline__ void put_two(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
@@ -345,22 +340,27 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             }
         }
         // Unaligned rows: every warp copies its own, the 16-byte granules that hold them, two
-        // turns ahead (rows that are not used stay out).
+        // turns ahead (rows that are not used stay out); 32 / ST lanes to a row.
         const auto fetch = [&](int it) {
             const int k = it * R + rank;
             if (k < ntiles) {
+                constexpr int LPR = 32 / ST;
                 const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
-                const int r0 = BWD ? TT - (warp + 1) * ST : warp * ST;  // the group's lowest row
-                const int n = min(CW, p.C - c0);
+                const int r = (BWD ? TT - (warp + 1) * ST : warp * ST) + lane / LPR;
                 uint8_t* d = sm + (it & 1) * SM::DATA;
                 const auto copy = [&](auto t, uint8_t* tile, const void* base, int back, int64_t s) {
-                    using E = Tile<decltype(t), TMA>;
-                    constexpr int GR = E::PITCH / 16;
-                    for (int q = lane; q < ST * GR; q += 32) {
-                        const int r = r0 + q / GR, o = q % GR * 16, row = row0 + r - back;
-                        if (row >= 0 && row0 + r < T_end && o < (int)E::bytes(base, row, s, c0, n))
-                            cp_async16(tile + r * E::PITCH + o, E::granule(base, row, s, c0) + o);
-                    }
+                    using E = decltype(t);
+                    constexpr int PITCH = Tile<E, TMA>::PITCH;
+                    if (row0 + r >= T_end || row0 + r - back < 0) return;
+                    const uintptr_t at = reinterpret_cast<uintptr_t>(
+                        static_cast<const E*>(base) + (int64_t)(row0 + r - back) * s + c0);
+                    const uintptr_t end = at + min(CW, p.C - c0) * (int)sizeof(E);
+                    uintptr_t from = (at & ~(uintptr_t)15) + lane % LPR * 16;
+                    uint8_t* to = tile + r * PITCH + lane % LPR * 16;
+#pragma unroll
+                    for (int o = 0; o < PITCH; o += LPR * 16)
+                        if (from + o < end)
+                            cp_async16(to + o, reinterpret_cast<const void*>(from + o));
                 };
                 copy(G(), d + SM::X, p.la, 0, p.las);
                 copy(IO(), d, p.x, 0, p.xs);
@@ -417,21 +417,30 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                     __syncwarp();
                 }
                 typename Pair<G>::Raw l[ST];
+                // (the shifts of unaligned rows, from the group's lowest row up)
+                const int low = BWD ? TT - (warp + 1) * ST : warp * ST;
+                uint32_t sl = 0, sx = 0, sh = 0;
+                if (!TMA) {
+                    sl = Tile<G, TMA>::shift(p.la, row0 + low, p.las, c0);
+                    sx = Tile<IO, TMA>::shift(p.x, row0 + low, p.xs, c0);
+                    if (BWD) sh = Tile<IO, TMA>::shift(p.h, row0 + low - 1, p.hs, c0);
+                }
 #pragma unroll
-                for (int j = 0; j < ST; ++j) {
-                    const int r = BWD ? TT - 1 - (warp * ST + j) : warp * ST + j;
-                    const int64_t t = row0 + r;
-                    l[j] = Tile<G, TMA>::at(d + SM::X, r, lane, p.la, t, p.las, c0);
-                    x[j] = Tile<IO, TMA>::at(d, r, lane, p.x, t, p.xs, c0);
-                    if (BWD)
-                        before[j] =
-                            Tile<IO, TMA>::at(d + SM::X + SM::L, r, lane, p.h, t - 1, p.hs, c0);
+                for (int i = 0; i < ST; ++i) {
+                    const int j = BWD ? ST - 1 - i : i, r = low + i;
+                    l[j] = Tile<G, TMA>::at(d + SM::X, r, lane, sl);
+                    x[j] = Tile<IO, TMA>::at(d, r, lane, sx);
+                    if (BWD) before[j] = Tile<IO, TMA>::at(d + SM::X + SM::L, r, lane, sh);
+                    if (!TMA) {
+                        sl = (sl + Tile<G, TMA>::shift_step(p.las)) & 15u;
+                        sx = (sx + Tile<IO, TMA>::shift_step(p.xs)) & 15u;
+                        if (BWD) sh = (sh + Tile<IO, TMA>::shift_step(p.hs)) & 15u;
+                    }
                 }
 #pragma unroll
                 for (int j = 0; j < ST; ++j) a[j] = exp2ch(Pair<G>::widen(l[j]));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[st]);  // the tile is in registers
-                if (!TMA) fetch(it + 2);
                 // the map of these ST rows (only what follows the last reset counts)
                 if (reset) {
 #pragma unroll
@@ -459,6 +468,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 const uint32_t bar = smem_u32(&joined[b]);
                 for (int r = 0; r < R; ++r) st_async(map_rank(to, r), v, map_rank(bar, r));
             }
+            if (!TMA && live) fetch(it + 2);  // (while the maps travel)
             mbar_wait_cluster(&joined[b], (it >> 1) & 1, abort_flag);
             float2 h = state;
 #pragma unroll 4
@@ -668,8 +678,13 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
         return wide ? launch_tiles<IO, G, BWD, true, 8, 16, 1>(p, stream)
                     : launch_tiles<IO, G, BWD, false, 8, ST, 1>(p, stream);
     }
+    // Unaligned tiles always come two at a time; smaller ones then, but for two streams of bf16, so
+    // as not to queue (32,768 x 3,001: fp32 gradients 449 us against 1713 us with 16 rows a warp,
+    // bf16 gradients 357 us against 709 us, fp32 forward 321 us against 379 us, bf16 forward 272 us
+    // against 250 us).
+    constexpr int ST = BWD || sizeof(IO) + sizeof(G) > 4 ? 8 : 16;
     return wide ? launch_tiles<IO, G, BWD, true, 4, 16, 3>(p, stream)
-                : launch_tiles<IO, G, BWD, false, 4, 16, 3>(p, stream);
+                : launch_tiles<IO, G, BWD, false, 4, ST, 3>(p, stream);
 }
 
 template <bool BWD>
