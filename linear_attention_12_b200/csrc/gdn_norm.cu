@@ -427,7 +427,9 @@ Access access_of(const NormParams& p, bool bf16) {
     }
     return wide ? WIDE : (pair ? PAIR : SINGLE);
 }
-bool is_plain(const NormParams& p, bool wide) { return wide && !p.centred && !p.has_bias; }
+bool is_plain(const NormParams& p, bool wide) {
+    return wide && !p.centred && !p.has_bias && !p.db_part;  // (dbias may be asked for without bias)
+}
 Shape backward_shape(int T, int H, int d, bool wide, bool bf16, bool plain) {
     return shape_of(T, H, d, wide, bf16, bwd_blocks(plain, wide && bf16), BWD_TOKENS);
 }

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 import os
 import threading
 
@@ -514,23 +515,26 @@ def _placed(fn):
     current stream), outputs and workspaces allocated there too.  With a ``stream`` of its
     own, every tensor given is kept from reuse until the work on that stream is done."""
 
+    name = next(iter(inspect.signature(fn).parameters))
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        first = args[0] if args else kw.get(name)
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise TypeError(f"{fn.__name__}: the first argument must be a CUDA tensor")
+            raise TypeError(f"{fn.__name__}: {name} must be a CUDA tensor")
         device = first.device
         if stream is None:
             if device.index == torch._C._cuda_getDevice():
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
             with torch.cuda.device(device):
-                return fn(first, *args, **kw)
+                return fn(*args, **kw)
         if stream.device != device:
             raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
                              f"{device}")
         # (a stream's context makes its device current as well)
         with torch.cuda.stream(stream):
-            out = fn(first, *args, **kw)
-        given = [first, *args, *kw.values()]
+            out = fn(*args, **kw)
+        given = [*args, *kw.values()]
         while given:
             t = given.pop()
             if isinstance(t, torch.Tensor) and t.is_cuda:

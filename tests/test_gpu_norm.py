@@ -195,6 +195,37 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
     assert all(torch.equal(p, q) for p, q in zip(first, held))
 
 
+def test_bias_gradient_without_a_bias():
+    """At the C level the gradient of a bias of zeros may be asked for."""
+    T, H, d = 50, 3, 128
+    x, dy, w, b, z = _case(T, H, d, BF16, 19, bias=False, per_head=False)
+    cx, cdy, cw, _, cz = _cuda(x, dy, w, b, z)
+    ref = gdn.group_norm_backward(cdy, cx, cw, torch.zeros_like(cw), cz)
+    L = gdn.lib()
+    ws = torch.empty(L.gdn_group_norm_backward_workspace_size(T, H, d, 1, gdn.GDN_BF16),
+                     dtype=torch.uint8, device="cuda")
+    dx, dz, dw, db = cx.clone(), cx.clone(), cw.clone(), cw.clone()
+    n = H * d
+    st = L.gdn_group_norm_backward(cdy.data_ptr(), n, cx.data_ptr(), n, cz.data_ptr(), n,
+                                   cw.data_ptr(), None, T, H, d, 1, 0, 1, 1e-6, gdn.GDN_BF16,
+                                   dx.data_ptr(), n, dz.data_ptr(), n, dw.data_ptr(), db.data_ptr(),
+                                   ws.data_ptr(), ws.numel(),
+                                   torch.cuda.current_stream().cuda_stream)
+    assert st == gdn.GDN_OK
+    torch.cuda.synchronize()
+    for p, q in zip((dx, dw, db, dz), ref):
+        assert torch.equal(p, q)
+
+
+def test_keywords_and_given_workspaces():
+    x, dy, w, b, z = _cuda(*_case(70, 5, 96, F32, 21))
+    ref = gdn.group_norm_backward(dy, x, w, b, z)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda").fill_(255)
+    got = gdn.group_norm_backward(dy=dy, x=x, weight=w, bias=b, z=z, workspace=ws)
+    assert all(torch.equal(p, q) for p, q in zip(ref, got))
+    assert torch.equal(gdn.group_norm(x=x, weight=w, bias=b, z=z), gdn.group_norm(x, w, b, z))
+
+
 def test_refusals():
     x, dy, w, b, z = _cuda(*_case(6, 2, 64, BF16, 17))
     with pytest.raises(ValueError):

@@ -1,4 +1,8 @@
 """gdn_scan, gdn_scan_backward and gdn_scan_step against the fp64 oracle."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -287,6 +291,39 @@ def test_same_bits_again_on_another_stream_and_in_a_graph(T, C):
     want = torch.exp(la[:2].float())
     ref = want * (want * h0 + x[:2].float()) + x[:2].float()
     torch.testing.assert_close(state, ref, rtol=1e-5, atol=1e-5)
+
+
+def test_first_call_inside_a_capture():
+    """A process whose first calls are captured (the kernels' attributes and the room for their
+    clusters are asked for then)."""
+    code = """
+import torch
+from linear_attention_12_b200 import gdn
+g = torch.Generator("cuda").manual_seed(1)
+x = torch.randn(3000, 320, generator=g, device="cuda")
+la = -torch.rand(3000, 320, generator=g, device="cuda")
+w = torch.ones(64, device="cuda")
+gdn.lib()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    h, hf = gdn.scan(x=x, log_alpha=la)
+    back = gdn.scan_backward(la, h, x)
+    y = gdn.group_norm(h.view(3000, 5, 64), w)
+    back += gdn.group_norm_backward(y, h.view(3000, 5, 64), w)[:2]
+graph.replay()
+torch.cuda.synchronize()
+held = (h, hf, y, *back)
+h, hf = gdn.scan(x, la)
+back = gdn.scan_backward(la, h, x)
+y = gdn.group_norm(h.view(3000, 5, 64), w)
+back += gdn.group_norm_backward(y, h.view(3000, 5, 64), w)[:2]
+assert all(torch.equal(p, q) for p, q in zip(held, (h, hf, y, *back)))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True,
+                         timeout=300)
+    assert out.stdout.strip().endswith("same"), out.stderr[-2000:]
 
 
 def test_two_calls_at_once():
