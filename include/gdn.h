@@ -556,8 +556,7 @@ typedef enum {
  *     n  = weight xh + bias
  *     y  = n act(z)   with a gate z,   y = act(n)   without
  *
- * (The pages name an output norm and a gate around the mixers and print no
- * formula.)
+ * (The pages print no formula for it; this is the norm's own definition.)
  *
  *   x, z, y   : [T, H, d] io_dtype; row strides over tokens, the H d columns of a
  *               token dense; z NULL for no gate.  1 <= d <= GDN_MAX_GROUP_DIM.

@@ -1,4 +1,5 @@
-"""B200-native Gated DeltaNet (GDN) layer: chunked prefill and decode step.
+"""B200-native Gated DeltaNet (GDN) layer: front end, chunked prefill, decode step and
+their gradients, the per-channel gated recurrence beside it and the norm behind both.
 
 The compute lives in ``libgdn.so`` (hand-written CUDA for sm_100a behind a
 C ABI declared in ``include/gdn.h``).  ``linear_attention_12_b200.gdn`` is a

@@ -8,8 +8,8 @@ Per token and head of ``x [T, H, d]``:
     n  = weight xh + bias
     y  = n act(z) with a gate z, act(n) without;   act = identity or silu
 
-The pages name an output norm and a gate and print no formula; this is the plain
-reading.  The gradients are the chain rule of these lines, written per element.
+The pages print no formula for it; this is the norm's own definition.  The gradients
+are the chain rule of these lines, written per element.
 """
 from __future__ import annotations
 
