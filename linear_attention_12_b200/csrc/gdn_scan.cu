@@ -394,9 +394,9 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             int last_reset = -1, first_emit = -1;
             float2 kept = make_float2(0.f, 0.f), kept_h0 = kept;
             // h (or u) of a row, from the row's before it in scan order
-            const auto step = [&](int j, float2 s) {
-                const float2 xj = Pair<IO>::widen(x[j]);
-                return BWD ? mul2(a[j], add2(s, xj)) : fma2(a[j], s, xj);
+            const auto step = [](float2 aj, typename Pair<IO>::Raw xj, float2 s) {
+                const float2 v = Pair<IO>::widen(xj);
+                return BWD ? mul2(aj, add2(s, v)) : fma2(aj, s, v);
             };
             if (live) {
                 if (mbar_wait(&full[st], (it >> two_stages) & 1, abort_flag)) {
@@ -445,12 +445,12 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 if (reset) {
 #pragma unroll
                     for (int j = 0; j < ST; ++j)
-                        mine.b = step(j, j == last_reset ? kept : mine.b);
+                        mine.b = step(a[j], x[j], j == last_reset ? kept : mine.b);
                     mine.a = make_float2(-1.f, -1.f);
                 } else {
 #pragma unroll
                     for (int j = 0; j < ST; ++j) {
-                        mine.b = step(j, mine.b);
+                        mine.b = step(a[j], x[j], mine.b);
                         mine.a = mul2(mine.a, a[j]);
                     }
                 }
@@ -485,7 +485,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             G* pg = BWD ? static_cast<G*>(p.dla) + (int64_t)(row0 + r0) * p.dlas + c : nullptr;
             // o: the row's output, g: its second one (the gradients' dlog_alpha)
             const auto run = [&](int j, float2& o, float2& g, float2 w) {
-                o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(j, h);
+                o = BWD ? add2(h, Pair<IO>::widen(x[j])) : step(a[j], x[j], h);
                 h = BWD ? mul2(a[j], o) : o;
                 if (BWD) g = mul2(h, w);
             };
@@ -683,7 +683,9 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
     // bf16 gradients 357 us against 709 us, fp32 forward 321 us against 379 us, bf16 forward 272 us
     // against 250 us).
     constexpr int ST = BWD || sizeof(IO) + sizeof(G) > 4 ? 8 : 16;
-    return wide ? launch_tiles<IO, G, BWD, true, 4, 16, 3>(p, stream)
+    // (the shared memory of three fp32 tiles leaves room for two blocks an SM: their registers then)
+    constexpr int MINB = BWD && sizeof(IO) == 4 ? 2 : 3;
+    return wide ? launch_tiles<IO, G, BWD, true, 4, 16, MINB>(p, stream)
                 : launch_tiles<IO, G, BWD, false, 4, ST, 3>(p, stream);
 }
 

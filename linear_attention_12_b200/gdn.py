@@ -477,7 +477,7 @@ def _expect(t, name, dtype, shape, device):
 def _rows(t, name, dtype, shape, device, cols) -> int:
     """Row stride of a token-major tensor whose rows of ``cols`` elements are dense (a column
     slice of a wider tensor will do); raises where it is not of this dtype, shape, device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
             and t.shape == shape and t.is_contiguous()):
         return cols
     _expect(t, name, dtype, shape, device)
@@ -494,16 +494,21 @@ def _rows(t, name, dtype, shape, device, cols) -> int:
 
 
 def _dense(t, name, dtype, shape, device):
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
             and t.shape == shape and t.is_contiguous()):
         return
     _expect(t, name, dtype, shape, device)
     raise ValueError(f"{name} must be contiguous")
 
 
-def _new(t):
-    """A dense tensor of t's shape, dtype and device."""
-    return torch.empty_like(t, memory_format=torch.contiguous_format, requires_grad=False)
+@functools.lru_cache(1024)
+def _norm_workspace(device_index, *sizes) -> int:
+    return lib().gdn_group_norm_backward_workspace_size(*sizes)
+
+
+@functools.lru_cache(1024)
+def _frontend_workspace(device_index, *sizes) -> int:
+    return lib().gdn_frontend_backward_workspace_size(*sizes)
 
 
 def _at(t):
@@ -596,7 +601,7 @@ def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_s
     if h0 is not None:
         _dense(h0, "h0", torch.float32, (N, *chans), dev)
     if h is None:
-        h, hs = _new(x), C
+        h, hs = torch.empty_like(x), C
     else:
         hs = _rows(h, "h", x.dtype, shape, dev, C)
     if h_final is not None:
@@ -626,11 +631,11 @@ def scan_backward(log_alpha, h, dh, h0=None, dh_final=None, cu_seqlens=None, *, 
         if t is not None:
             _dense(t, name, torch.float32, (N, *chans), dev)
     if dx is None:
-        dx, dxs = _new(h), C
+        dx, dxs = torch.empty_like(h), C
     else:
         dxs = _rows(dx, "dx", h.dtype, shape, dev, C)
     if dlog_alpha is None:
-        dlog_alpha, dlas = _new(log_alpha), C
+        dlog_alpha, dlas = torch.empty_like(log_alpha), C
     else:
         dlas = _rows(dlog_alpha, "dlog_alpha", log_alpha.dtype, shape, dev, C)
     dh0 = torch.empty((N, *chans), dtype=torch.float32, device=dev) if want_dh0 else None
@@ -652,7 +657,7 @@ def scan_step(x, log_alpha, state, *, h=None):
     las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
     _dense(state, "state", torch.float32, shape, dev)
     if h is None:
-        h, hs = _new(x), C
+        h, hs = torch.empty_like(x), C
     else:
         hs = _rows(h, "h", x.dtype, shape, dev, C)
     st = lib().gdn_scan_step(x.data_ptr(), xs, log_alpha.data_ptr(), las, state.data_ptr(), B, C,
@@ -689,7 +694,7 @@ def group_norm(x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6
     other calls."""
     T, H, d, C, wh, io, xs, zs = _norm_args(x, weight, bias, z)
     if y is None:
-        y, ys = _new(x), C
+        y, ys = torch.empty_like(x), C
     else:
         ys = _rows(y, "y", x.dtype, x.shape, x.device, C)
     st = lib().gdn_group_norm(x.data_ptr(), xs, _at(z), zs, weight.data_ptr(), _at(bias), T, H, d,
@@ -712,7 +717,7 @@ def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="si
     dev = x.device
     dys = _rows(dy, "dy", x.dtype, x.shape, dev, C)
     if dx is None:
-        dx, dxs = _new(x), C
+        dx, dxs = torch.empty_like(x), C
     else:
         dxs = _rows(dx, "dx", x.dtype, x.shape, dev, C)
     if z is None and dz is not None:
@@ -720,16 +725,15 @@ def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="si
     dzs = 0
     if z is not None:
         if dz is None:
-            dz = _new(x)
+            dz = torch.empty_like(x)
             dzs = C
         else:
             dzs = _rows(dz, "dz", x.dtype, x.shape, dev, C)
-    dw = _new(weight)
-    db = None if bias is None else _new(weight)
+    dw = torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(weight)
     L = lib()
     if workspace is None:
-        need = L.gdn_group_norm_backward_workspace_size(T, H, d, wh, io)
-        workspace = _workspace(None, need, dev)
+        workspace = _workspace(None, _norm_workspace(dev.index, T, H, d, wh, io), dev)
     else:
         _workspace(workspace, 0, dev)
     st = L.gdn_group_norm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _at(z), zs,
@@ -771,12 +775,11 @@ def frontend_backward(q_raw, k_raw, v_raw, conv_w, a, b, dq, dk, dv, dlog_alpha,
     _dense(dbeta, "dbeta", f32, gs, dev)
     _dense(conv_w, "conv_w", f32, ((2 * H_qk + H_v) * dk_, 4), dev)
     _, _, _, N, cu = _scan_sizes(q_raw, cu_seqlens, dev)
-    dq_raw, dk_raw, dv_raw, dw, da, db = (_new(q_raw), _new(k_raw), _new(v_raw), _new(conv_w),
-                                          _new(a), _new(b))
+    dq_raw, dk_raw, dv_raw, dw, da, db = map(torch.empty_like, (q_raw, k_raw, v_raw, conv_w, a, b))
     L = lib()
     if workspace is None:
-        workspace = _workspace(None, L.gdn_frontend_backward_workspace_size(T, H_qk, H_v, dk_, dv_,
-                                                                            io), dev)
+        need = _frontend_workspace(dev.index, T, H_qk, H_v, dk_, dv_, io)
+        workspace = _workspace(None, need, dev)
     else:
         _workspace(workspace, 0, dev)
     st = L.gdn_frontend_backward(
