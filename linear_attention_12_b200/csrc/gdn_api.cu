@@ -29,6 +29,15 @@ cudaError_t read_and_clear_status(unsigned int* status, cudaStream_t stream) {
     return cudaStreamSynchronize(stream);
 }
 
+int known_sms() {
+    static std::atomic<int> known[kKnownDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kKnownDevices) return device_sms();
+    int sms = known[dev].load(std::memory_order_relaxed);
+    if (sms == 0) known[dev].store(sms = device_sms(), std::memory_order_relaxed);
+    return sms;
+}
+
 // Waits (bounded) on an mbarrier that nothing arrives at: the wait gives up,
 // records the timeout in the status word, and every thread returns.
 __global__ void selftest_bounded_wait_kernel() {

@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(FG_LAST)
 // the last warps of q and k ran alone: 485 us against 420 us for 32,768 tokens of 16/48 bf16
 // heads).
 void frontend_grad_runs(int T, int H_qk, int H_v, GradRuns& qk, GradRuns& v) {
-    const long long warps = (long long)device_sms() * FG_BLOCKS * FG_WARPS;
+    const long long warps = (long long)known_sms() * FG_BLOCKS * FG_WARPS;
     const auto cut = [T](long long runs) {
         const long long most = ((long long)T + 31) / 32;
         if (runs > most) runs = most;

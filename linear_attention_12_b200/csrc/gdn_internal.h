@@ -25,6 +25,8 @@ constexpr int kKnownDevices = 64;
 
 // SM count of the current device (148 when there is none).
 int device_sms();
+// The same, remembered for each device (for calls that ask several times).
+int known_sms();
 
 // Segments per sequence the prefill uses when the caller leaves it to the
 // library: 1 unless splitting the sequences fills more of the SMs.

@@ -404,7 +404,7 @@ Shape shape_of(int T, int H, int d, bool wide, bool bf16, int blocks_per_sm, int
     const long long gpb = NT / s.lg, groups = (long long)T * H;
     const long long need = (groups + gpb * tokens - 1) / (gpb * tokens);
     const long long least = (H + gpb - 1) / gpb;
-    long long blocks = (long long)device_sms() * blocks_per_sm;
+    long long blocks = (long long)known_sms() * blocks_per_sm;
     if (blocks > need) blocks = need;
     if (blocks < least) blocks = least;
     s.blocks = (int)blocks;

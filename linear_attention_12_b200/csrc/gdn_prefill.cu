@@ -47,8 +47,6 @@
 // the chunk loop also votes on whether all of its threads are still healthy,
 // so a timeout makes the CTA leave the loop together, drain its in-flight
 // copies (bounded) and exit.
-#include <atomic>
-
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -1568,18 +1566,13 @@ size_t prefill_workspace_bytes(int N, int T, int H_qk, int H_v, bool bf16, int P
 }
 
 int device_sms() {
-    // (asked several times per call: remembered for each device)
-    static std::atomic<int> known[kKnownDevices];
     int dev = 0, sms = 0;
-    const bool got = cudaGetDevice(&dev) == cudaSuccess;
-    if (got && dev < kKnownDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0)
-        return sms;
-    if (!got || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
         sms <= 0) {
         cudaGetLastError();  // no device: clear the error, assume a B200
         return 148;
     }
-    if (dev < kKnownDevices) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
 }
 

@@ -671,7 +671,7 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
                       (!BWD || (wide_rows(p.h, p.hs, e) && wide_rows(p.dla, p.dlas, ge)));
     // Few channels leave one block an SM or less: larger tiles then, for fewer turns of the
     // cluster (131,072 x 128 bf16 forward: 217 us against 315 us).
-    const bool few = ((long long)p.C + CW - 1) / CW * 8 <= device_sms();
+    const bool few = ((long long)p.C + CW - 1) / CW * 8 <= known_sms();
     if (few) {
         // (16 rows a warp do not fit the shared memory where three unaligned fp32 tiles are held)
         constexpr int ST = BWD && sizeof(IO) + sizeof(G) == 8 ? 8 : 16;
