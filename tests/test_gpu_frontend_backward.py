@@ -143,6 +143,27 @@ def test_nothing_crosses_a_boundary():
         assert torch.equal(p[:20], q[:20]) and torch.equal(p[50:], q[50:])
 
 
+def test_large_offsets():
+    """Values whose element offsets pass 2^31: the last sequence's gradients are those it has
+    alone (each of its rows is the same arithmetic, whichever run takes it)."""
+    T, Hq, Hv, at = 88000, 1, 192, 87400
+    g = torch.Generator("cuda").manual_seed(3)
+    rnd = lambda *s, **k: torch.randn(*s, generator=g, device="cuda", **k)
+    assert at * Hv * 128 > 2 ** 31
+    q, k, dq, dk = (rnd(T, Hq, 128, dtype=BF16) for _ in range(4))
+    v, dv = (rnd(T, Hv, 128, dtype=BF16) for _ in range(2))
+    a, b, dla, dbe = (rnd(T, Hv) for _ in range(4))
+    w = rnd((2 * Hq + Hv) * 128, 4)
+    cu = torch.tensor([0, at, T], dtype=torch.int32, device="cuda")
+    got = gdn.frontend_backward(q, k, v, w, a, b, dq, dk, dv, dla, dbe, cu, act="silu")
+    tail = [t[at:].contiguous() for t in (q, k, v, a, b, dq, dk, dv, dla, dbe)]
+    ref = gdn.frontend_backward(*tail[:3], w, *tail[3:], act="silu")
+    for i, (p, r) in enumerate(zip(got, ref)):
+        if i != 3:
+            assert torch.equal(p[at:], r)
+    assert got[3].isfinite().all()
+
+
 def test_no_tokens():
     e = lambda *s: torch.empty(*s, device="cuda")
     w = torch.randn(3 * 128, 4, device="cuda")

@@ -195,6 +195,22 @@ def test_same_bits_again_on_another_stream_and_in_a_graph():
     assert all(torch.equal(p, q) for p, q in zip(first, held))
 
 
+def test_large_offsets():
+    """Rows whose element offsets pass 2^31."""
+    T, H, d, stride = 70000, 1, 64, 40000
+    wide = torch.zeros(T * stride, dtype=BF16, device="cuda")
+    cut = [torch.as_strided(wide, (T, H, d), (stride, d, 1), 64 * i) for i in range(5)]
+    assert (T - 1) * stride > 2 ** 31
+    x, dy, w, b, z = _cuda(*_case(T, H, d, BF16, 23))
+    for s, v in zip(cut, (x, z, dy)):
+        s.copy_(v)
+    y = gdn.group_norm(cut[0], w, b, cut[1], y=cut[3])
+    assert torch.equal(y, gdn.group_norm(x, w, b, z))
+    got = gdn.group_norm_backward(cut[2], cut[0], w, b, cut[1], dx=cut[3], dz=cut[4])
+    ref = gdn.group_norm_backward(dy, x, w, b, z)
+    assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
 def test_bias_gradient_without_a_bias():
     """At the C level the gradient of a bias of zeros may be asked for."""
     T, H, d = 50, 3, 128
