@@ -1,4 +1,5 @@
-"""Build ``libgdn.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_100a.
+"""Build ``libgdn.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and
+``_gdn_torch.so`` (the binding's argument checks, host code against PyTorch's headers).
 
 Usage: ``python -m linear_attention_12_b200.build [--force] [--verbose]``.
 The library is written next to this file so that it travels with the
@@ -12,12 +13,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libgdn.so")
+BINDING = os.path.join(HERE, "_gdn_torch.so")
+BINDING_SRC = os.path.join(CSRC, "gdn_torch.cpp")
 BUILD_DIR = os.path.join(HERE, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -43,8 +47,34 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """Compile ``csrc/gdn_torch.cpp`` into ``_gdn_torch.so``; return its path."""
+    deps = (BINDING_SRC, os.path.join(ROOT, "include", "gdn.h"))
+    if (not force and os.path.exists(BINDING)
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
+        return BINDING
+    import torch
+    t = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    for d in (os.path.join(t, "include"), os.path.join(t, "include", "torch", "csrc", "api", "include"),
+              os.path.join(cuda, "include"), sysconfig.get_paths()["include"]):
+        cmd += ["-I", d]
+    cmd += [BINDING_SRC, "-o", tmp, "-L", os.path.join(t, "lib"), "-ltorch_python", "-ltorch_cuda",
+            "-ltorch_cpu", "-ltorch", "-lc10_cuda", "-lc10"]
+    if verbose:
+        print(" ".join(cmd), file=sys.stderr)
+    subprocess.check_call(cmd)
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every ``csrc/*.cu`` into ``libgdn.so``; return its path."""
+    """Compile every ``csrc/*.cu`` into ``libgdn.so``, and the binding's ``_gdn_torch.so``;
+    return the library's path."""
+    build_binding(force=force, verbose=verbose)
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()

@@ -1,14 +1,12 @@
 """ctypes binding of ``libgdn.so`` (C ABI in ``include/gdn.h``).
 
-Argument marshalling only: every step of the computation runs in the CUDA
-library.  PyTorch provides device memory and the current stream.  There is no
+Argument marshalling only (the scan, norm and front-end gradient calls' in
+``csrc/gdn_torch.cpp``): every step of the computation runs in the CUDA library.  PyTorch provides device memory and the current stream.  There is no
 fallback: if the library is missing, or a call fails, an exception is raised.
 """
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import os
 import threading
 
@@ -446,7 +444,48 @@ def frontend_decode_step(q_raw, k_raw, v_raw, conv_w, a, b, conv_state, *, act="
     return q, k, v, la, be
 
 
-_DTYPES = {torch.bfloat16: GDN_BF16, torch.float32: GDN_F32}
+# ---- the calls below go through _gdn_torch (csrc/gdn_torch.cpp): the same marshalling in C++ ----
+_NATIVE = ("gdn_scan", "gdn_scan_backward", "gdn_scan_step", "gdn_group_norm",
+           "gdn_group_norm_backward", "gdn_group_norm_backward_workspace_size",
+           "gdn_frontend_backward", "gdn_frontend_backward_workspace_size")
+_ext = None
+
+
+def _native():
+    """The compiled argument checks (once).  Raises if they have not been built."""
+    global _ext
+    L = lib()
+    with _lock:
+        if _ext is None:
+            try:
+                from . import _gdn_torch
+            except ImportError as e:
+                raise RuntimeError("_gdn_torch.so is missing or does not fit this PyTorch: build it "
+                                   "with `python -m linear_attention_12_b200.build`") from e
+            _gdn_torch.bind(*(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _NATIVE))
+            _ext = _gdn_torch
+    return _ext
+
+
+def _run(name, args, stream):
+    """One call of ``_gdn_torch`` on the current stream of its tensors' device, or on ``stream``:
+    outputs and workspaces are allocated there too, and every tensor given is kept from reuse
+    until the work on that stream is done."""
+    fn = getattr(_ext or _native(), name)
+    if stream is None:
+        out = fn(*args)
+    else:
+        given = [t for t in args if isinstance(t, torch.Tensor) and t.is_cuda]
+        for t in given:
+            if t.device != stream.device:
+                raise ValueError(f"{name}: the stream is on {stream.device}, a tensor on {t.device}")
+        with torch.cuda.stream(stream):
+            out = fn(*args)
+        for t in given:
+            t.record_stream(stream)
+    if type(out) is int:
+        raise GDNError(out, "gdn_" + name)
+    return out
 
 
 def _choice(value, choices, name):
@@ -456,135 +495,8 @@ def _choice(value, choices, name):
     return got
 
 
-def _dtype_of(t, name):
-    got = _DTYPES.get(t.dtype) if isinstance(t, torch.Tensor) else None
-    if got is None:
-        raise TypeError(f"{name} must be a bfloat16 or float32 tensor")
-    return got
-
-
-def _expect(t, name, dtype, shape, device):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-
-
-def _rows(t, name, dtype, shape, device, cols) -> int:
-    """Row stride of a token-major tensor whose rows of ``cols`` elements are dense (a column
-    slice of a wider tensor will do); raises where it is not of this dtype, shape, device."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
-            and t.shape == shape and t.is_contiguous()):
-        return cols
-    _expect(t, name, dtype, shape, device)
-    dense = 1
-    for i in range(len(shape) - 1, 0, -1):
-        if shape[i] != 1 and t.stride(i) != dense:
-            raise ValueError(f"the rows of {name} must be dense, got strides {t.stride()}")
-        dense *= shape[i]
-    if shape[0] <= 1:
-        return cols
-    if t.stride(0) < cols:
-        raise ValueError(f"the rows of {name} overlap: strides {t.stride()}")
-    return t.stride(0)
-
-
-def _dense(t, name, dtype, shape, device):
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index
-            and t.shape == shape and t.is_contiguous()):
-        return
-    _expect(t, name, dtype, shape, device)
-    raise ValueError(f"{name} must be contiguous")
-
-
-@functools.lru_cache(1024)
-def _norm_workspace(device_index, *sizes) -> int:
-    return lib().gdn_group_norm_backward_workspace_size(*sizes)
-
-
-@functools.lru_cache(1024)
-def _frontend_workspace(device_index, *sizes) -> int:
-    return lib().gdn_frontend_backward_workspace_size(*sizes)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _placed(fn):
-    """Run ``fn`` on the device of its first argument and on ``stream`` (None: that device's
-    current stream), outputs and workspaces allocated there too.  With a ``stream`` of its
-    own, every tensor given is kept from reuse until the work on that stream is done."""
-
-    name = next(iter(inspect.signature(fn).parameters))
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        first = args[0] if args else kw.get(name)
-        if not isinstance(first, torch.Tensor) or not first.is_cuda:
-            raise TypeError(f"{fn.__name__}: {name} must be a CUDA tensor")
-        device = first.device
-        if stream is None:
-            if device.index == torch._C._cuda_getDevice():
-                return fn(*args, **kw)
-            with torch.cuda.device(device):
-                return fn(*args, **kw)
-        if stream.device != device:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on "
-                             f"{device}")
-        # (a stream's context makes its device current as well)
-        with torch.cuda.stream(stream):
-            out = fn(*args, **kw)
-        given = [*args, *kw.values()]
-        while given:
-            t = given.pop()
-            if isinstance(t, torch.Tensor) and t.is_cuda:
-                t.record_stream(stream)
-            elif isinstance(t, (tuple, list)):
-                given.extend(t)
-        return out
-
-    return call
-
-
-def _here(device):
-    """The current stream of a device, as a cudaStream_t (what
-    ``torch.cuda.current_stream(device).cuda_stream`` says, without the objects)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=device) if need else None
-    _dense(workspace, "workspace", workspace.dtype, workspace.shape, device)
-    return workspace
-
-
-def _nbytes(t):
-    return 0 if t is None else t.numel() * t.element_size()
-
-
-def _scan_sizes(first, cu_seqlens, device):
-    """(T, C, the shape of a token's channels, N, pointer of cu_seqlens)."""
-    shape = first.shape
-    if len(shape) < 2:
-        raise ValueError(f"expected [T, ...channels], got {tuple(shape)}")
-    chans = shape[1:]
-    C = chans[0] if len(chans) == 1 else chans.numel()
-    if cu_seqlens is None:
-        return shape[0], C, chans, 1, None
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
-        raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
-    _dense(cu_seqlens, "cu_seqlens", torch.int32, cu_seqlens.shape, device)
-    return shape[0], C, chans, cu_seqlens.numel() - 1, cu_seqlens.data_ptr()
-
-
-@_placed
-def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_state=True):
+def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_state=True,
+         stream=None):
     """The gated linear recurrence ``h_t = exp(log_alpha_t) h_{t-1} + x_t`` per channel over
     packed sequences (gdn_scan).
 
@@ -592,205 +504,59 @@ def scan(x, log_alpha, h0=None, cu_seqlens=None, *, h=None, h_final=None, want_s
     of the same shape, bf16 or fp32; ``h0`` [N, C] fp32 or None for zeros; ``cu_seqlens`` int32
     [N + 1] on the device or None for one sequence.  x, log_alpha and h may be column slices
     of wider tensors.  Returns ``(h, h_final)``: h in x's type, h_final [N, C] fp32 (None if
-    not wanted).  Rows from ``cu_seqlens[-1]`` on stay unwritten.  ``stream``: as for the
-    other calls."""
-    io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
-    T, C, chans, N, cu = _scan_sizes(x, cu_seqlens, dev)
-    xs = _rows(x, "x", x.dtype, shape, dev, C)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
-    if h0 is not None:
-        _dense(h0, "h0", torch.float32, (N, *chans), dev)
-    if h is None:
-        h, hs = torch.empty_like(x), C
-    else:
-        hs = _rows(h, "h", x.dtype, shape, dev, C)
-    if h_final is not None:
-        _dense(h_final, "h_final", torch.float32, (N, *chans), dev)
-    elif want_state:
-        h_final = torch.empty((N, *chans), dtype=torch.float32, device=dev)
-    st = lib().gdn_scan(x.data_ptr(), xs, log_alpha.data_ptr(), las, _at(h0), cu, N, T, C, io, gate,
-                        h.data_ptr(), hs, _at(h_final), _here(dev))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_scan")
-    return h, h_final
+    not wanted).  Rows from ``cu_seqlens[-1]`` on stay unwritten."""
+    return _run("scan", (x, log_alpha, h0, cu_seqlens, h, h_final, want_state), stream)
 
 
-@_placed
 def scan_backward(log_alpha, h, dh, h0=None, dh_final=None, cu_seqlens=None, *, dx=None,
-                  dlog_alpha=None, want_dh0=True):
+                  dlog_alpha=None, want_dh0=True, stream=None):
     """Gradients of ``<dh, h> + <dh_final, h_final>`` for :func:`scan` (gdn_scan_backward);
     ``h`` is the scan's output.
 
     Returns ``(dx, dlog_alpha, dh0)``: dx in h's type, dlog_alpha in log_alpha's, dh0 [N, C]
     fp32 (None if not wanted)."""
-    io, gate, dev, shape = _dtype_of(h, "h"), _dtype_of(log_alpha, "log_alpha"), h.device, h.shape
-    T, C, chans, N, cu = _scan_sizes(h, cu_seqlens, dev)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
-    hs, dhs = _rows(h, "h", h.dtype, shape, dev, C), _rows(dh, "dh", h.dtype, shape, dev, C)
-    for t, name in ((h0, "h0"), (dh_final, "dh_final")):
-        if t is not None:
-            _dense(t, name, torch.float32, (N, *chans), dev)
-    if dx is None:
-        dx, dxs = torch.empty_like(h), C
-    else:
-        dxs = _rows(dx, "dx", h.dtype, shape, dev, C)
-    if dlog_alpha is None:
-        dlog_alpha, dlas = torch.empty_like(log_alpha), C
-    else:
-        dlas = _rows(dlog_alpha, "dlog_alpha", log_alpha.dtype, shape, dev, C)
-    dh0 = torch.empty((N, *chans), dtype=torch.float32, device=dev) if want_dh0 else None
-    st = lib().gdn_scan_backward(log_alpha.data_ptr(), las, h.data_ptr(), hs, dh.data_ptr(), dhs,
-                                 _at(h0), _at(dh_final), cu, N, T, C, io, gate, dx.data_ptr(), dxs,
-                                 dlog_alpha.data_ptr(), dlas, _at(dh0), _here(dev))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_scan_backward")
-    return dx, dlog_alpha, dh0
+    return _run("scan_backward", (log_alpha, h, dh, h0, dh_final, cu_seqlens, dx, dlog_alpha,
+                                  want_dh0), stream)
 
 
-@_placed
-def scan_step(x, log_alpha, state, *, h=None):
+def scan_step(x, log_alpha, state, *, h=None, stream=None):
     """One token of each of B sequences (gdn_scan_step): ``state`` [B, C] fp32 is updated in
     place to ``exp(log_alpha) state + x``.  Returns ``h``, the new state in x's type."""
-    io, gate, dev, shape = _dtype_of(x, "x"), _dtype_of(log_alpha, "log_alpha"), x.device, x.shape
-    B, C, _, _, _ = _scan_sizes(x, None, dev)
-    xs = _rows(x, "x", x.dtype, shape, dev, C)
-    las = _rows(log_alpha, "log_alpha", log_alpha.dtype, shape, dev, C)
-    _dense(state, "state", torch.float32, shape, dev)
-    if h is None:
-        h, hs = torch.empty_like(x), C
-    else:
-        hs = _rows(h, "h", x.dtype, shape, dev, C)
-    st = lib().gdn_scan_step(x.data_ptr(), xs, log_alpha.data_ptr(), las, state.data_ptr(), B, C,
-                             io, gate, h.data_ptr(), hs, _here(dev))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_scan_step")
-    return h
+    return _run("scan_step", (x, log_alpha, state, h), stream)
 
 
-def _norm_args(x, weight, bias, z):
-    if x.dim() != 3:
-        raise ValueError(f"x must be [T, H, d], got {tuple(x.shape)}")
-    io = _dtype_of(x, "x")
-    T, H, d = x.shape
-    dev = x.device
-    shared = (d,)
-    if not isinstance(weight, torch.Tensor) or weight.shape not in (shared, (H, d)):
-        raise ValueError(f"weight must have shape ({d},) or ({H}, {d})")
-    _dense(weight, "weight", torch.float32, weight.shape, dev)
-    if bias is not None:
-        _dense(bias, "bias", torch.float32, weight.shape, dev)
-    C = H * d
-    return (T, H, d, C, 1 if weight.dim() == 1 else H, io, _rows(x, "x", x.dtype, x.shape, dev, C),
-            0 if z is None else _rows(z, "z", x.dtype, x.shape, dev, C))
-
-
-@_placed
-def group_norm(x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6, y=None):
+def group_norm(x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6, y=None,
+               stream=None):
     """Norm over every head of a mixer's output, with its activation or activated gate
     (gdn_group_norm): ``y = n act(z)`` with a gate ``z``, ``act(n)`` without, where
     ``n = weight xh + bias`` and ``xh`` is x [T, H, d] normalised over d -- ``norm`` "rms"
     or "mean" (centred).  ``weight`` and ``bias``: fp32 [d] or [H, d].  x, z and y may be
-    column slices of wider tensors.  Returns ``y`` in x's type.  ``stream``: as for the
-    other calls."""
-    T, H, d, C, wh, io, xs, zs = _norm_args(x, weight, bias, z)
-    if y is None:
-        y, ys = torch.empty_like(x), C
-    else:
-        ys = _rows(y, "y", x.dtype, x.shape, x.device, C)
-    st = lib().gdn_group_norm(x.data_ptr(), xs, _at(z), zs, weight.data_ptr(), _at(bias), T, H, d,
-                              wh, _choice(norm, _NORMS, "norm"), _choice(act, _ACTS, "act"), eps,
-                              io, y.data_ptr(), ys, _here(x.device))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_group_norm")
-    return y
+    column slices of wider tensors.  Returns ``y`` in x's type."""
+    return _run("group_norm", (x, weight, bias, z, _choice(norm, _NORMS, "norm"),
+                               _choice(act, _ACTS, "act"), eps, y), stream)
 
 
-@_placed
 def group_norm_backward(dy, x, weight, bias=None, z=None, *, norm="rms", act="silu", eps=1e-6,
-                        dx=None, dz=None, workspace=None):
+                        dx=None, dz=None, workspace=None, stream=None):
     """Gradients of ``<dy, y>`` for :func:`group_norm` (gdn_group_norm_backward).
 
     Returns ``(dx, dweight, dbias, dz)``: dx and dz in x's type, dweight and dbias fp32 of
     weight's shape; dbias None without a bias, dz None without a gate.  ``dx`` and ``dz``
     may be given (column slices of wider tensors will do)."""
-    T, H, d, C, wh, io, xs, zs = _norm_args(x, weight, bias, z)
-    dev = x.device
-    dys = _rows(dy, "dy", x.dtype, x.shape, dev, C)
-    if dx is None:
-        dx, dxs = torch.empty_like(x), C
-    else:
-        dxs = _rows(dx, "dx", x.dtype, x.shape, dev, C)
-    if z is None and dz is not None:
-        raise ValueError("dz without z")
-    dzs = 0
-    if z is not None:
-        if dz is None:
-            dz = torch.empty_like(x)
-            dzs = C
-        else:
-            dzs = _rows(dz, "dz", x.dtype, x.shape, dev, C)
-    dw = torch.empty_like(weight)
-    db = None if bias is None else torch.empty_like(weight)
-    L = lib()
-    if workspace is None:
-        workspace = _workspace(None, _norm_workspace(dev.index, T, H, d, wh, io), dev)
-    else:
-        _workspace(workspace, 0, dev)
-    st = L.gdn_group_norm_backward(dy.data_ptr(), dys, x.data_ptr(), xs, _at(z), zs,
-                                   weight.data_ptr(), _at(bias), T, H, d, wh,
-                                   _choice(norm, _NORMS, "norm"), _choice(act, _ACTS, "act"), eps,
-                                   io, dx.data_ptr(), dxs, _at(dz), dzs, dw.data_ptr(), _at(db),
-                                   _at(workspace), _nbytes(workspace), _here(dev))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_group_norm_backward")
-    return dx, dw, db, dz
+    return _run("group_norm_backward", (dy, x, weight, bias, z, _choice(norm, _NORMS, "norm"),
+                                        _choice(act, _ACTS, "act"), eps, dx, dz, workspace), stream)
 
 
-@_placed
 def frontend_backward(q_raw, k_raw, v_raw, conv_w, a, b, dq, dk, dv, dlog_alpha, dbeta,
-                      cu_seqlens=None, *, act="none", eps=1e-6, workspace=None):
+                      cu_seqlens=None, *, act="none", eps=1e-6, workspace=None, stream=None):
     """Gradients of :func:`frontend` (gdn_frontend_backward): from those of q, k, v, log_alpha
     and beta (``prefill_backward``'s results) to those of its inputs.
 
     Returns ``(dq_raw, dk_raw, dv_raw, dconv_w, da, db)``: the first three in the inputs'
     type, the others fp32.  Rows from ``cu_seqlens[-1]`` on stay unwritten."""
-    if q_raw.dim() != 3 or v_raw.dim() != 3:
-        raise ValueError("q_raw, k_raw and v_raw must be [T, H, d]")
-    io, dt, dev, qs, vs = (_dtype_of(q_raw, "q_raw"), q_raw.dtype, q_raw.device, q_raw.shape,
-                           v_raw.shape)
-    T, H_qk, dk_ = qs
-    _, H_v, dv_ = vs
-    if vs[0] != T:
-        raise ValueError(f"v_raw has {vs[0]} tokens, q_raw {T}")
-    gs, f32 = (T, H_v), torch.float32
-    _dense(q_raw, "q_raw", dt, qs, dev)
-    _dense(k_raw, "k_raw", dt, qs, dev)
-    _dense(v_raw, "v_raw", dt, vs, dev)
-    _dense(dq, "dq", dt, qs, dev)
-    _dense(dk, "dk", dt, qs, dev)
-    _dense(dv, "dv", dt, vs, dev)
-    _dense(a, "a", f32, gs, dev)
-    _dense(b, "b", f32, gs, dev)
-    _dense(dlog_alpha, "dlog_alpha", f32, gs, dev)
-    _dense(dbeta, "dbeta", f32, gs, dev)
-    _dense(conv_w, "conv_w", f32, ((2 * H_qk + H_v) * dk_, 4), dev)
-    _, _, _, N, cu = _scan_sizes(q_raw, cu_seqlens, dev)
-    dq_raw, dk_raw, dv_raw, dw, da, db = map(torch.empty_like, (q_raw, k_raw, v_raw, conv_w, a, b))
-    L = lib()
-    if workspace is None:
-        need = _frontend_workspace(dev.index, T, H_qk, H_v, dk_, dv_, io)
-        workspace = _workspace(None, need, dev)
-    else:
-        _workspace(workspace, 0, dev)
-    st = L.gdn_frontend_backward(
-        q_raw.data_ptr(), k_raw.data_ptr(), v_raw.data_ptr(), conv_w.data_ptr(), a.data_ptr(),
-        b.data_ptr(), cu, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), dlog_alpha.data_ptr(),
-        dbeta.data_ptr(), N, T, H_qk, H_v, dk_, dv_, io, _choice(act, _ACTS, "act"), eps,
-        dq_raw.data_ptr(), dk_raw.data_ptr(), dv_raw.data_ptr(), dw.data_ptr(), da.data_ptr(),
-        db.data_ptr(), _at(workspace), _nbytes(workspace), _here(dev))
-    if st != GDN_OK:
-        raise GDNError(st, "gdn_frontend_backward")
-    return dq_raw, dk_raw, dv_raw, dw, da, db
+    return _run("frontend_backward", (q_raw, k_raw, v_raw, conv_w, a, b, dq, dk, dv, dlog_alpha,
+                                      dbeta, cu_seqlens, _choice(act, _ACTS, "act"), eps, workspace),
+                stream)
 
 
 def selftest_bounded_wait(stream=None) -> None:
