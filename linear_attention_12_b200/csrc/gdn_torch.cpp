@@ -167,6 +167,12 @@ int64_t channels(const Tensor& x) {
     return C;
 }
 
+bool truth(PyObject* o) {
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();
+    return v != 0;
+}
+
 PyObject* status(gdn_status st) { return PyLong_FromLong(st); }
 
 // A tuple of tensors (an undefined one: None).
@@ -213,7 +219,7 @@ PyObject* scan(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor hf;
     if (a[5] != Py_None)
         hf = dense(a[5], "h_final", at::kFloat, states, dev);
-    else if (PyObject_IsTrue(a[6]))
+    else if (truth(a[6]))
         hf = fresh(states, at::kFloat, dev);
     const gdn_status st =
         lib.scan(x.data_ptr(), xs, la.data_ptr(), las, h0, cu, N, size32(x.size(0), "T"),
@@ -245,7 +251,7 @@ PyObject* scan_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     int64_t dxs, dlas;
     const Tensor dx = output(a[6], "dx", h.scalar_type(), shape, dev, C, dxs);
     const Tensor dla = output(a[7], "dlog_alpha", la.scalar_type(), shape, dev, C, dlas);
-    const Tensor dh0 = PyObject_IsTrue(a[8]) ? fresh(states, at::kFloat, dev) : Tensor();
+    const Tensor dh0 = truth(a[8]) ? fresh(states, at::kFloat, dev) : Tensor();
     const gdn_status st = lib.scan_backward(
         la.data_ptr(), las, h.data_ptr(), hs, dh.data_ptr(), dhs, h0, dhf, cu, N,
         size32(h.size(0), "T"), size32(C, "C"), io, gate, dx.data_ptr(), dxs, dla.data_ptr(), dlas,
