@@ -128,6 +128,27 @@ __device__ __forceinline__ float2 exp2ch(float2 v) {
     return r;
 }
 
+// A lane's two channels of a row: neighbours, or 32 apart.
+template <bool TILED>
+__device__ __forceinline__ void put_both(float* p, float2 v) {
+    if (TILED) {
+        put_two(p, v);
+    } else {
+        p[0] = v.x;
+        p[32] = v.y;
+    }
+}
+template <bool TILED>
+__device__ __forceinline__ void put_both(__nv_bfloat16* p, float2 v) {
+    if (TILED) {
+        put_two(p, v);
+    } else {
+        const uint32_t u = pack_bf16x2(v.x, v.y);
+        reinterpret_cast<uint16_t*>(p)[0] = (uint16_t)u;
+        reinterpret_cast<uint16_t*>(p)[32] = (uint16_t)(u >> 16);
+    }
+}
+
 // A map s -> A s + B of two channels.
 struct Map {
     float2 a, b;
@@ -507,15 +528,15 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             };
             // Three forms of the same loop: rows without marks, groups with one boundary (no branch
             // inside: the rows' instructions interleave, which halves the time), and the rest.
-            if (TMA && !(reset | emit) && row0 + TT <= T_end && c0 + CW <= p.C) {
+            if (!(reset | emit) && row0 + TT <= T_end && c0 + CW <= p.C) {
 #pragma unroll
                 for (int j = 0; j < ST; ++j) {
                     float2 o, g;
                     run(j, o, g, Pair<IO>::widen(before[BWD ? j : 0]));
-                    put_two(po, o);
+                    put_both<TMA>(po, o);
                     po += DIR * p.outs;
                     if (BWD) {
-                        put_two(pg, g);
+                        put_both<TMA>(pg, g);
                         pg += DIR * p.dlas;
                     }
                 }
