@@ -460,8 +460,6 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
 #pragma unroll
                 for (int j = 0; j < ST; ++j) a[j] = exp2ch(Pair<G>::widen(l[j]));
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);  // the tile is in registers
                 // the map of these ST rows (only what follows the last reset counts)
                 if (reset) {
 #pragma unroll
@@ -477,6 +475,13 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
             }
             agg[(b * WARPS + warp) * 32 + lane] = as4(mine);
+            // The tile is free again.  (Not before this store, which needs every value read from
+            // it: given up right behind the reads, a tile was now and then overwritten under one
+            // of them when the instructions in between came from a cold cache.)
+            if (live) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[st]);
+            }
             bar_sync<SCAN_BAR, WARPS * 32>();
             // the map of the time groups before this one, within the tile
             Map pre{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};

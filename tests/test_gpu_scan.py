@@ -326,6 +326,28 @@ print("same")
     assert out.stdout.strip().endswith("same"), out.stderr[-2000:]
 
 
+@pytest.mark.parametrize("io,gate", TYPES)
+def test_same_bits_from_a_cold_cache(io, gate):
+    """The data and the code out of the caches before every call: the timing between the
+    copies into a tile and the reads from it is another one then."""
+    T, C, N = 4000, 2048, 20
+    g = torch.Generator().manual_seed(31)
+    cu = [0, *sorted(torch.randint(0, T + 1, (N - 1,), generator=g).tolist()), T]
+    x, la, h0, dh, df, cu = _cuda(*_case(T, C, cu, io, gate, 31))
+    ref = gdn.scan(x, la, h0, cu)
+    back = gdn.scan_backward(la, ref[0], dh, h0, df, cu)
+    flush = torch.empty(160 << 20, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for k in range(600):
+        flush.fill_(k % 256)
+        got = gdn.scan(x, la, h0, cu)
+        flush.fill_(k % 255)
+        got += gdn.scan_backward(la, ref[0], dh, h0, df, cu)
+        for p, q in zip(got, ref + back):
+            differ += (p != q).any()
+    assert int(differ) == 0
+
+
 def test_two_calls_at_once():
     """Calls on two streams that overlap do not disturb one another."""
     one = _cuda(*_case(5000, 256, [0, 1000, 5000], BF16, BF16, 16))
