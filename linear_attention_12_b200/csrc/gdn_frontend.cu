@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(32)
 // rows feeds the convolution, three partial rows of dx wait for the tokens ahead of them,
 // and dw runs in registers.  Runs overlap by the three rows behind and ahead of them.
 //
-// Every warp keeps two tiles of rows (x and the output gradient) on their way by TMA into its
+// Every warp keeps three tiles of rows (x and the output gradient) on their way by TMA into its
 // own part of shared memory; within a tile nothing but the window joins the rows, so their
 // latencies overlap.  The arithmetic goes two channels to an instruction.  A warp holds a whole
 // head, for the sums over a head of q or k and because rows of 256 bytes keep the memory busy
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(32)
 // than the warps bring (32,768 tokens of 16/48 bf16 heads: 428 us against 395 us).
 constexpr int FG_WARPS = 1;                     // per block: each on its own, and its slot free at its end
 constexpr int FG_BLOCKS = 12;                   // blocks per SM: all runs at once
-constexpr int FG_STAGES = 2;                    // (a power of two)
+constexpr int FG_STAGES = 4;                    // of a ring (a power of two), three on their way
 constexpr int FG_HALF = 8 * FD * 2;             // bytes of a stage's rows of x: 8 of bf16, 4 of fp32
 constexpr int FG_RING = FG_STAGES * 2 * FG_HALF;  // bytes of a warp's ring
 constexpr int FG_SMEM = FG_WARPS * (FG_RING + FG_STAGES * 8) + 16;
@@ -517,7 +517,7 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
         tma_load_2d(d, mx, c0, ta + i * ROWS, bar);
         tma_load_2d(d + FG_HALF, mg, c0, ta + i * ROWS, bar);
     };
-    for (int i = 0; i < STAGES; ++i) fetch(i);
+    for (int i = 0; i < STAGES - 1; ++i) fetch(i);
 
     // the sequence of token ta, and where the next one starts
     int n = 0, first = 0, next = T_end;
@@ -549,7 +549,7 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
         if (!mbar_wait(&full[(i & (STAGES - 1))], (i / STAGES) & 1, abort_flag)) {
             // the copies may still land: wait for them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
-            for (int k = i; k < min(i + STAGES, tiles); ++k)
+            for (int k = i; k < min(i + STAGES - 1, tiles); ++k)
                 while (!mbar_try_wait(smem_u32(&full[(k & (STAGES - 1))]), (k / STAGES) & 1) &&
                        globaltimer() - ts < kWaitLimitNs) {
                 }
@@ -587,8 +587,10 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
                                                          dx, rs, a.eps);
             }
         }
-        __syncwarp();  // everyone has read the tile
-        fetch(i + STAGES);
+        // Into the place of the tile before this one: everything read from that has gone into
+        // the rows stored since (this one's last rows still wait in registers).
+        __syncwarp();
+        fetch(i + STAGES - 1);
     }
     grad_flush(s, te, tb, dx, rs);
 }

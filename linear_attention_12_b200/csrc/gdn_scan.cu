@@ -683,7 +683,7 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     // A second tile on its way hides the first one's latency.  The gradients' five streams
     // stand more in flight badly: past what the memory system needs it only lengthens the
     // queues, clusters progress unevenly and the last ones run alone.  32,768 x 6144 bf16
-    // gradients took 410 us with 18.9 MB in flight and 331 us with 9.4 MB; the forward with
+    // gradients took 410 us with 18.9 MB in flight and 339 us with 9.4 MB; the forward with
     // fp32 gates took 246 us with 18.9 MB and 270 us with 9.4 MB.
     const int two = !BWD || !TMA || groups * R * (2ll * SM::DATA) <= (15 << 20);
     return cudaLaunchKernelEx(&cfg, kernel, mx, ml, mh, p, R, two);
