@@ -277,7 +277,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&full[i], TMA ? 2 : 1);  // the copies, and the rows' marks
-            mbar_init(&empty[i], WARPS);
+            mbar_init(&empty[i], 1);
             mbar_init(&joined[i], 1);
         }
         *abort_flag = 0;
@@ -475,14 +475,14 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 }
             }
             agg[(b * WARPS + warp) * 32 + lane] = as4(mine);
-            // The tile is free again.  (Not before this store, which needs every value read from
-            // it: given up right behind the reads, a tile was now and then overwritten under one
-            // of them when the instructions in between came from a cold cache.)
-            if (live) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[st]);
-            }
+            // The tile is free again behind the warps' barrier, which no read of it can pass, with
+            // each lane's reads ordered before the next copy, another proxy's write, by a fence.
+            // (An arrive of every warp right behind its reads did not hold them: a tile was now
+            // and then overwritten under the last of them when the code behind came from a cold
+            // cache, and the gradients' h is not even needed before the second run.)
+            if (TMA) fence_proxy_async_smem();
             bar_sync<SCAN_BAR, WARPS * 32>();
+            if (live && threadIdx.x == 0) mbar_arrive(&empty[st]);
             // the map of the time groups before this one, within the tile
             Map pre{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
             for (int q = 0; q < warp; ++q)

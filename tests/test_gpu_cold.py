@@ -1,0 +1,57 @@
+"""The same bits from a cold cache.  With the data and the code out of the caches the timing
+between the copies into a tile and the reads from it is another one: a tile that is handed back
+too early is overwritten under its reads then, and almost never otherwise."""
+import pytest
+import torch
+
+from linear_attention_12_b200 import gdn
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(autouse=True)
+def _status_clean():
+    yield
+    assert gdn.last_device_error() == gdn.GDN_OK
+
+
+def _cu(T, N, seed):
+    g = torch.Generator().manual_seed(seed)
+    cuts = sorted(torch.randint(0, T + 1, (N - 1,), generator=g).tolist())
+    return torch.tensor([0, *cuts, T], dtype=torch.int32, device="cuda")
+
+
+def _differing(call, times):
+    """How many of `times` cold calls differ in any bit from the first."""
+    ref = call()
+    flush = torch.empty(160 << 20, dtype=torch.uint8, device="cuda")
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for k in range(times):
+        flush.fill_(k % 256)
+        differ += torch.stack([(p != q).any() for p, q in zip(call(), ref)]).any()
+    return int(differ)
+
+
+# 8-warp tiles and 4-warp tiles, each from aligned rows (by TMA) and from odd ones (granules)
+@pytest.mark.parametrize("C", [512, 515, 1280, 2051])
+@pytest.mark.parametrize("io,gate", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+def test_scan_gradients(io, gate, C):
+    T, N = 4000, 20
+    g = torch.Generator("cuda").manual_seed(C)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    la = -torch.rand(T, C, generator=g, device="cuda").to(gate)
+    h, dh, h0, df, cu = rnd(T, C).to(io), rnd(T, C).to(io), rnd(N, C), rnd(N, C), _cu(T, N, C)
+    assert _differing(lambda: gdn.scan_backward(la, h, dh, h0, df, cu), 200) == 0
+
+
+@pytest.mark.parametrize("C", [512, 515, 1280, 2051])
+@pytest.mark.parametrize("io,gate", [(BF16, BF16), (BF16, F32), (F32, BF16), (F32, F32)])
+def test_scan(io, gate, C):
+    T, N = 4000, 20
+    g = torch.Generator("cuda").manual_seed(C)
+    la = -torch.rand(T, C, generator=g, device="cuda").to(gate)
+    x = torch.randn(T, C, generator=g, device="cuda").to(io)
+    h0, cu = torch.randn(N, C, generator=g, device="cuda"), _cu(T, N, C)
+    assert _differing(lambda: gdn.scan(x, la, h0, cu), 100) == 0
