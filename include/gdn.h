@@ -404,6 +404,20 @@ GDN_API gdn_status gdn_get_last_device_error(void *stream);
 GDN_API gdn_status gdn_selftest_bounded_wait(void *stream);
 
 /*
+ * gdn_selftest_scan_wait -- the same for the scan, whose blocks wait for one
+ * another: enqueue a gdn_scan (backward 0) or gdn_scan_backward (1) of one
+ * sequence of T fp32 rows of C channels, of which tile `tile` (rows of 64 or 128
+ * tokens, counted in the direction of the scan) never reaches shared memory, with
+ * a wait limit of about 20 ms.  Every block of that tile's cluster unwinds and the
+ * kernel returns normally; the outputs are void, and gdn_get_last_device_error
+ * returns GDN_ERR_TIMEOUT -- GDN_OK if there is no such tile.
+ *
+ *   buffers : fp32 [5, T, C], dense: log_alpha, x (or h), h (or dh), dx, dlog_alpha.
+ */
+GDN_API gdn_status gdn_selftest_scan_wait(int32_t backward, float *buffers, int32_t T, int32_t C,
+                                          int32_t tile, void *stream);
+
+/*
  * gdn_frontend -- the step before the recurrence: turn a layer's raw q, k, v
  * projections and gate pre-activations into gdn_prefill's inputs.
  *

@@ -694,6 +694,30 @@ gdn_status gdn_selftest_bounded_wait(void* stream) {
     return cudaGetLastError() == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
 }
 
+gdn_status gdn_selftest_scan_wait(int32_t backward, float* buffers, int32_t T, int32_t C,
+                                  int32_t tile, void* stream) {
+    gdn_status st = check_scan(nullptr, 1, T, C, GDN_F32, GDN_F32);
+    if (st != GDN_OK) return st;
+    if (T == 0 || tile < 0 || !buffers || !aligned(buffers, 4)) return GDN_ERR_INVALID_ARG;
+    st = check_device();
+    if (st != GDN_OK) return st;
+    float* b[5];
+    for (int i = 0; i < 5; ++i) b[i] = buffers + (size_t)i * T * C;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (backward) {
+        gdn::ScanGradArgs a{b[0], b[1], b[2], nullptr, nullptr, nullptr, b[3], b[4], nullptr,
+                            C, C, C, C, C, 1, T, C};
+        a.drop = tile;
+        e = gdn::launch_scan_backward(a, false, false, s);
+    } else {
+        gdn::ScanArgs a{b[1], b[0], nullptr, nullptr, b[2], nullptr, C, C, C, 1, T, C};
+        a.drop = tile;
+        e = gdn::launch_scan(a, false, false, s);
+    }
+    return e == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
 gdn_status gdn_get_last_device_error(void* stream) {
     unsigned int status = 0u;
     if (gdn::read_and_clear_status(&status, static_cast<cudaStream_t>(stream)) != cudaSuccess)

@@ -57,6 +57,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float v) {
 constexpr int CW = 64;             // channels of a tile
 constexpr int MAX_CLUSTER = 16;    // (above 8 only where the device grants it)
 constexpr int SCAN_BAR = 1;        // named barrier of the consumer warps
+constexpr unsigned long long kTestWaitNs = 20000000ull;  // limit of the waits that a test lets run out
 
 struct ScanParams {
     const void *x, *la, *h;        // forward: x; gradients: dh, and h the forward's output
@@ -66,6 +67,8 @@ struct ScanParams {
     float* last;                   // h_final, or dh0
     int64_t xs, las, hs, outs, dlas;
     int N, T, C;
+    int drop = -1;  // a test's: this tile (in scan order) never comes
+    unsigned long long limit = kWaitLimitNs;
 };
 
 // Two neighbouring channels, as stored (bf16 pairs stay packed in one register) and widened.
@@ -203,7 +206,7 @@ __device__ __forceinline__ void st_async(uint32_t addr, float4 v, uint32_t bar) 
         "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(bar)
         : "memory");
 }
-// mbar_wait for data that other blocks of the cluster wrote.
+// mbar_wait for data that other blocks of the cluster wrote.  It gives up by its limit alone.
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t ok;
     asm volatile(
@@ -216,20 +219,28 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
     return ok != 0;
 }
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile int* abort) {
+                                                  volatile int* abort, unsigned long long limit) {
     const uint32_t addr = smem_u32(bar);
     if (mbar_try_wait_cluster(addr, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (;;) {
         if (mbar_try_wait_cluster(addr, parity)) return true;
-        if (*abort) return false;
-        if (globaltimer() - t0 > kWaitLimitNs) {
+        if (globaltimer() - t0 > limit) {
             atomicOr(&g_status, GDN_DEV_TIMEOUT);
             *abort = 1;
             return false;
         }
     }
 }
+
+// When a wait runs out, all of a cluster unwinds, and its output is void (the status says so):
+//   * The producer issues nothing more, and waits for what it has issued.
+//   * A block's consumer warps learn of it together, at the barrier of their next map, send
+//     nothing more and leave.
+//   * The other blocks never see that turn's maps complete, give up on them in turn (by a
+//     longer limit than the wait that a block may have before it sends) and leave in the same way.
+// Nobody ends before all have come to the last barrier of the cluster, and who waited in vain
+// for the others' maps sent its own long before, so none is on its way any more.
 
 // Shared memory of a block.
 template <typename IO, typename G, bool BWD, bool TMA, int WARPS, int ST>
@@ -287,11 +298,14 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
 
     if (warp == WARPS) {
         // ---- producer: tiles by TMA, and the rows where sequences start and end ----
-        int it = 0;
+        int it = 0;  // tiles issued
         for (; it * R + rank < ntiles; ++it) {
             const int st = it & two_stages, turn = it >> two_stages, k = it * R + rank;
             const int row0 = (BWD ? ntiles - 1 - k : k) * TT;
-            if (turn > 0) mbar_wait(&empty[st], (turn - 1) & 1, abort_flag);
+            if (k == p.drop) break;
+            if (turn > 0 && !__all_sync(0xffffffffu, mbar_wait(&empty[st], (turn - 1) & 1,
+                                                               abort_flag, p.limit)))
+                break;
             if (TMA && lane == 0) {
                 uint8_t* d = sm + st * SM::DATA;
                 mbar_arrive_expect_tx(&full[st], SM::DATA);
@@ -332,15 +346,10 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             __syncwarp();
             if (lane == 0) mbar_arrive(&full[st]);
         }
-        if (*abort_flag && lane == 0) {
-            // copies may still be landing: let them (bounded) before the block ends
-            const unsigned long long ts = globaltimer();
+        // the last copies have landed (bounded) before the block ends, whatever ended the loop
+        if (lane == 0)
             for (int j = max(0, it - 1 - two_stages); j < it; ++j)
-                while (!mbar_try_wait(smem_u32(&full[j & two_stages]), (j >> two_stages) & 1) &&
-                       globaltimer() - ts < kWaitLimitNs) {
-                }
-        }
-        __syncwarp();
+                mbar_wait_drain(&full[j & two_stages], (j >> two_stages) & 1);
     } else {
         // ---- consumers ----
         constexpr int NEXT = TMA ? 1 : 32;  // a lane's second channel
@@ -393,6 +402,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             for (int it = 0; it < 2; ++it) fetch(it);
 
         float2 state = make_float2(0.f, 0.f);  // entering the R tiles of this iteration
+        bool lost = false;                     // a wait has run out
         for (int it = 0; it < iters; ++it) {
             const int st = it & two_stages, k = it * R + rank, b = it & 1;
             const bool live = k < ntiles;
@@ -420,7 +430,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 return BWD ? mul2(aj, add2(s, v)) : fma2(aj, s, v);
             };
             if (live) {
-                if (mbar_wait(&full[st], (it >> two_stages) & 1, abort_flag)) {
+                lost = lost || !mbar_wait(&full[st], (it >> two_stages) & 1, abort_flag, p.limit);
+                if (!lost) {
                     reset = m.reset[warp];
                     emit = m.emit[warp];
                 }
@@ -481,7 +492,8 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
             // and then overwritten under the last of them when the code behind came from a cold
             // cache, and the gradients' h is not even needed before the second run.)
             if (TMA) fence_proxy_async_smem();
-            bar_sync<SCAN_BAR, WARPS * 32>();
+            __syncwarp();
+            if (!bar_and<SCAN_BAR, WARPS * 32>(!lost)) break;
             if (live && threadIdx.x == 0) mbar_arrive(&empty[st]);
             // the map of the time groups before this one, within the tile
             Map pre{make_float2(1.f, 1.f), make_float2(0.f, 0.f)};
@@ -495,7 +507,10 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                 for (int r = 0; r < R; ++r) st_async(map_rank(to, r), v, map_rank(bar, r));
             }
             if (!TMA && live) fetch(it + 2);  // (while the maps travel)
-            mbar_wait_cluster(&joined[b], (it >> 1) & 1, abort_flag);
+            if (!mbar_wait_cluster(&joined[b], (it >> 1) & 1, abort_flag, 2 * p.limit)) {
+                lost = true;
+                continue;
+            }
             float2 h = state;
 #pragma unroll 4
             for (int r = 0; r < R; ++r) {
@@ -575,6 +590,7 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
         }
         cp_async_wait<0>();
     }
+    __syncwarp();
     cluster_sync();  // nobody ends while others may still send to it
 }
 
@@ -756,6 +772,7 @@ cudaError_t launch_scan(const ScanArgs& a, bool bf16, bool gate_bf16, cudaStream
     p.x = a.x, p.la = a.la, p.init = a.h0, p.cu = a.cu_seqlens, p.out = a.h, p.last = a.h_final;
     p.xs = a.x_stride, p.las = a.la_stride, p.outs = a.h_stride;
     p.N = a.N, p.T = a.T, p.C = a.C;
+    if (a.drop >= 0) p.drop = a.drop, p.limit = kTestWaitNs;
     return launch_direction<false>(p, bf16, gate_bf16, stream);
 }
 
@@ -767,6 +784,7 @@ cudaError_t launch_scan_backward(const ScanGradArgs& a, bool bf16, bool gate_bf1
     p.xs = a.dh_stride, p.las = a.la_stride, p.hs = a.h_stride, p.outs = a.dx_stride;
     p.dlas = a.dla_stride;
     p.N = a.N, p.T = a.T, p.C = a.C;
+    if (a.drop >= 0) p.drop = a.drop, p.limit = kTestWaitNs;
     return launch_direction<true>(p, bf16, gate_bf16, stream);
 }
 

@@ -98,6 +98,8 @@ SIGNATURES = {
     "gdn_frontend_backward_workspace_size": (_c.c_size_t, [_c.c_int32] * 5 + [_c.c_int]),
     "gdn_get_last_device_error": (_c.c_int, [_c.c_void_p]),
     "gdn_selftest_bounded_wait": (_c.c_int, [_c.c_void_p]),
+    "gdn_selftest_scan_wait": (_c.c_int, [_c.c_int32, _c.c_void_p] + [_c.c_int32] * 3 +
+                               [_c.c_void_p]),
     "gdn_status_string": (_c.c_char_p, [_c.c_int]),
     "gdn_version": (_c.c_int32, []),
 }
@@ -564,6 +566,18 @@ def selftest_bounded_wait(stream=None) -> None:
     st = lib().gdn_selftest_bounded_wait(_stream_handle(stream))
     if st != GDN_OK:
         raise GDNError(st, "gdn_selftest_bounded_wait")
+
+
+def selftest_scan_wait(buffers, tile, *, backward=False, stream=None) -> None:
+    """Enqueue a scan over ``buffers`` [5, T, C] fp32 whose tile ``tile`` never comes
+    (gdn_selftest_scan_wait): its waits run out and the kernel unwinds."""
+    _check(buffers, "buffers", torch.float32)
+    if buffers.dim() != 3 or buffers.shape[0] != 5:
+        raise ValueError(f"buffers must be [5, T, C], got {tuple(buffers.shape)}")
+    st = lib().gdn_selftest_scan_wait(int(bool(backward)), _ptr(buffers), buffers.shape[1],
+                                      buffers.shape[2], int(tile), _stream_handle(stream))
+    if st != GDN_OK:
+        raise GDNError(st, "gdn_selftest_scan_wait")
 
 
 def last_device_error(stream=None) -> int:
