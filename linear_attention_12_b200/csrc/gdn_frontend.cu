@@ -588,7 +588,9 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
             }
         }
         // Into the place of the tile before this one: everything read from that has gone into
-        // the rows stored since (this one's last rows still wait in registers).
+        // the rows stored since (this one's last rows still wait in registers), and each lane
+        // orders its reads before the copy, which comes through another proxy.
+        fence_proxy_async_smem();
         __syncwarp();
         fetch(i + STAGES - 1);
     }

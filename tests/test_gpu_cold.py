@@ -55,3 +55,17 @@ def test_scan(io, gate, C):
     x = torch.randn(T, C, generator=g, device="cuda").to(io)
     h0, cu = torch.randn(N, C, generator=g, device="cuda"), _cu(T, N, C)
     assert _differing(lambda: gdn.scan(x, la, h0, cu), 100) == 0
+
+
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("io", [BF16, F32])
+@pytest.mark.parametrize("T,N,Hq,Hv", [(4000, 20, 4, 12), (3000, 1, 1, 2), (9000, 6, 2, 6)])
+def test_frontend_gradients(T, N, Hq, Hv, io, act):
+    g = torch.Generator("cuda").manual_seed(T)
+    rnd = lambda *s, dt=io: torch.randn(*s, generator=g, device="cuda").to(dt)
+    raw = [rnd(T, Hq, 128), rnd(T, Hq, 128), rnd(T, Hv, 128), rnd((2 * Hq + Hv) * 128, 4, dt=F32),
+           rnd(T, Hv, dt=F32), rnd(T, Hv, dt=F32)]
+    grads = [rnd(T, Hq, 128), rnd(T, Hq, 128), rnd(T, Hv, 128), rnd(T, Hv, dt=F32),
+             rnd(T, Hv, dt=F32)]
+    cu = _cu(T, N, T)
+    assert _differing(lambda: gdn.frontend_backward(*raw, *grads, cu, act=act), 150) == 0
