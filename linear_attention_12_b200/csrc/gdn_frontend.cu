@@ -546,7 +546,9 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
     };
 
     for (int i = 0; i < tiles; ++i) {
-        if (!mbar_wait(&full[(i & (STAGES - 1))], (i / STAGES) & 1, abort_flag)) {
+        // (the lanes give up together: those that went on would wait for the others in a shuffle)
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait(&full[(i & (STAGES - 1))], (i / STAGES) & 1, abort_flag))) {
             // the copies may still land: wait for them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
             for (int k = i; k < min(i + STAGES - 1, tiles); ++k)
