@@ -475,8 +475,9 @@ GDN_API gdn_status gdn_frontend_decode_step(const void *q_raw, const void *k_raw
  * output a slice of its gradient.  Their data pointers need the alignment of
  * their element type; 16-byte aligned pointers with row strides that are
  * multiples of 16 bytes take the wide (vector or TMA) path, others a slower one
- * with the same results up to the order of sums.  Outputs must not overlap
- * inputs unless a call says so.
+ * with the same results up to the order of sums.  Of an input, nothing ahead of
+ * its first element or behind its last one is read; the bytes between two rows may
+ * be, and are never used.  Outputs must not overlap inputs unless a call says so.
  */
 
 /*

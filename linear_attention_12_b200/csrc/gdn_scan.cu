@@ -14,6 +14,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_common.cuh"
+#include "gdn_granules.h"
 #include "gdn_internal.h"
 #include "gdn_tiles.cuh"
 
@@ -174,9 +175,11 @@ __device__ __forceinline__ float2 apply(const Map& q, float2 s) {
     return q.a.x < 0.f ? q.b : fma2(q.a, s, q.b);
 }
 
-// Asynchronous 16-byte copies of a thread, in groups.
-__device__ __forceinline__ void cp_async16(void* to, const void* from) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from)
+// Asynchronous copies of a thread, in groups: 16 bytes, of which `bytes` are read and the others
+// zeros.
+__device__ __forceinline__ void cp_async16(void* to, const void* from, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)), "l"(from),
+                 "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -382,15 +385,19 @@ __global__ void __launch_bounds__((WARPS + 1) * 32, MINB)
                     using E = decltype(t);
                     constexpr int PITCH = Tile<E, TMA>::PITCH;
                     if (row0 + r >= T_end || row0 + r - back < 0) return;
+                    const E* whole = static_cast<const E*>(base);
                     const uintptr_t at = reinterpret_cast<uintptr_t>(
-                        static_cast<const E*>(base) + (int64_t)(row0 + r - back) * s + c0);
-                    const uintptr_t end = at + min(CW, p.C - c0) * (int)sizeof(E);
-                    uintptr_t from = (at & ~(uintptr_t)15) + lane % LPR * 16;
-                    uint8_t* to = tile + r * PITCH + lane % LPR * 16;
-#pragma unroll
-                    for (int o = 0; o < PITCH; o += LPR * 16)
-                        if (from + o < end)
-                            cp_async16(to + o, reinterpret_cast<const void*>(from + o));
+                        whole + (int64_t)(row0 + r - back) * s + c0);
+                    const uint8_t* from = reinterpret_cast<const uint8_t*>(at & ~(uintptr_t)15);
+                    uint8_t* to = tile + r * PITCH;
+                    copy_granules<E, LPR, (PITCH / 16 + LPR - 1) / LPR>(
+                        at, at + min(CW, p.C - c0) * (int)sizeof(E),
+                        reinterpret_cast<uintptr_t>(whole),
+                        reinterpret_cast<uintptr_t>(whole + (int64_t)(p.T - 1) * s + p.C),
+                        lane % LPR, [&](int o, int bytes) { cp_async16(to + o, from + o, bytes); },
+                        [&](int o) {
+                            *reinterpret_cast<E*>(to + o) = *reinterpret_cast<const E*>(from + o);
+                        });
                 };
                 copy(G(), d + SM::X, p.la, 0, p.las);
                 copy(IO(), d, p.x, 0, p.xs);
