@@ -1,5 +1,6 @@
-"""Build ``libgdn.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and
-``_gdn_torch.so`` (the binding's argument checks, host code against PyTorch's headers).
+"""Build ``libgdn.so`` (the C-ABI CUDA library) in-tree with nvcc for sm_100a, and, where
+PyTorch is installed, ``_gdn_torch.so`` (the binding's argument checks, host code against
+PyTorch's headers).
 
 Usage: ``python -m linear_attention_12_b200.build [--force] [--verbose]``.
 The library is written next to this file so that it travels with the
@@ -9,6 +10,8 @@ from __future__ import annotations
 
 import argparse
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -47,11 +50,23 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_version():
+    """The installed PyTorch's version, or None."""
+    try:
+        return importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return "unknown" if importlib.util.find_spec("torch") else None
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """Compile ``csrc/gdn_torch.cpp`` into ``_gdn_torch.so``; return its path."""
     deps = (BINDING_SRC, os.path.join(ROOT, "include", "gdn.h"))
+    # (it fits the PyTorch and the Python it was compiled against)
+    against = f"torch {_torch_version()}, {sysconfig.get_config_var('SOABI')}\n"
+    stamp = os.path.join(BUILD_DIR, "_gdn_torch.txt")
     if (not force and os.path.exists(BINDING)
-            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)):
+            and all(os.path.getmtime(d) <= os.path.getmtime(BINDING) for d in deps)
+            and os.path.exists(stamp) and open(stamp).read() == against):
         return BINDING
     import torch
     t = os.path.dirname(torch.__file__)
@@ -68,13 +83,29 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         print(" ".join(cmd), file=sys.stderr)
     subprocess.check_call(cmd)
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    with open(stamp, "w") as f:
+        f.write(against)
     return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile every ``csrc/*.cu`` into ``libgdn.so``, and the binding's ``_gdn_torch.so``;
-    return the library's path."""
-    build_binding(force=force, verbose=verbose)
+    """Compile every ``csrc/*.cu`` into ``libgdn.so``, then the binding's ``_gdn_torch.so``
+    (where there is a PyTorch for it); return the library's path."""
+    lib = build_library(force=force, verbose=verbose, ptxas_info=ptxas_info)
+    if _torch_version() is None:
+        print("no PyTorch: built the C library without _gdn_torch.so", file=sys.stderr)
+        return lib
+    try:
+        build_binding(force=force, verbose=verbose)
+    except Exception as e:
+        raise RuntimeError(f"{lib} is built, but the Python binding's _gdn_torch.so could not be "
+                           f"compiled: {e}") from e
+    return lib
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    """Compile every ``csrc/*.cu`` into ``libgdn.so``; return its path."""
     if not force and not _stale():
         return LIB
     nvcc = _nvcc()
