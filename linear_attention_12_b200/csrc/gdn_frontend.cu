@@ -471,7 +471,8 @@ __device__ __forceinline__ void grad_rows(GradState<P>& s, int t, const IO* xs, 
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
             const float r = rsqrtf(su[i].x + eps);
-            const float2 r2 = both(r), k = both(-r * r * r * su[i].y);
+            // (r^3 alone leaves fp32 for rows far from unit size; r <u, dout> does not)
+            const float2 r2 = both(r), k = both(-r * (r * (r * su[i].y)));
 #pragma unroll
             for (int c = 0; c < P; ++c) dy[i].c[c] = fma2(u[i].c[c], k, mul2(r2, dy[i].c[c]));
         }
