@@ -325,12 +325,11 @@ __global__ void __launch_bounds__(32)
 // (with rows of 128 bytes v's part took 246 us instead of 210 us even with its arithmetic left
 // out).  12 warps an SM at 168 registers: with 128 registers and 16 warps the spills cost more
 // than the warps bring (32,768 tokens of 16/48 bf16 heads: 428 us against 395 us).
-constexpr int FG_WARPS = 1;                     // per block: each on its own, and its slot free at its end
-constexpr int FG_BLOCKS = 12;                   // blocks per SM: all runs at once
+constexpr int FG_BLOCKS = 12;                   // blocks (of one warp) per SM: all runs at once
 constexpr int FG_STAGES = 4;                    // of a ring (a power of two), three on their way
 constexpr int FG_HALF = 8 * FD * 2;             // bytes of a stage's rows of x: 8 of bf16, 4 of fp32
 constexpr int FG_RING = FG_STAGES * 2 * FG_HALF;  // bytes of a warp's ring
-constexpr int FG_SMEM = FG_WARPS * (FG_RING + FG_STAGES * 8) + 16;
+constexpr int FG_SMEM = FG_RING + FG_STAGES * 8 + 16;
 
 // Runs of a kind of head: `runs` of `len` tokens each, and their partial sums of dw
 // [runs, the kind's channels, 4].
@@ -346,106 +345,82 @@ struct FrontendGradMaps {
     CUtensorMap x[3], dout[3];
 };
 
-// A lane's channels.
-template <int P>
+// A lane's channels: 2 P neighbours.
+constexpr int P = 2;
 struct Chans {
     float2 c[P];
 };
-template <int P>
-__device__ __forceinline__ Chans<P> zeros() {
-    Chans<P> r;
+__device__ __forceinline__ Chans zeros() {
+    Chans r;
 #pragma unroll
     for (int i = 0; i < P; ++i) r.c[i] = both(0.f);
     return r;
 }
-template <int P>
-__device__ __forceinline__ Chans<P> fma_c(const Chans<P>& a, const Chans<P>& b, const Chans<P>& c) {
-    Chans<P> r;
+__device__ __forceinline__ Chans fma_c(const Chans& a, const Chans& b, const Chans& c) {
+    Chans r;
 #pragma unroll
     for (int i = 0; i < P; ++i) r.c[i] = fma2(a.c[i], b.c[i], c.c[i]);
     return r;
 }
-template <int P>
-__device__ __forceinline__ Chans<P> mul_c(const Chans<P>& a, const Chans<P>& b) {
-    Chans<P> r;
+__device__ __forceinline__ Chans mul_c(const Chans& a, const Chans& b) {
+    Chans r;
 #pragma unroll
     for (int i = 0; i < P; ++i) r.c[i] = mul2(a.c[i], b.c[i]);
     return r;
 }
-template <int P>
-__device__ __forceinline__ float dot_c(const Chans<P>& a, const Chans<P>& b) {
+__device__ __forceinline__ float dot_c(const Chans& a, const Chans& b) {
     float2 s = mul2(a.c[0], b.c[0]);
 #pragma unroll
     for (int i = 1; i < P; ++i) s = fma2(a.c[i], b.c[i], s);
     return s.x + s.y;
 }
-template <int P>
-__device__ __forceinline__ Chans<P> load_c(const __nv_bfloat16* p) {
-    uint32_t u[P];
-    if constexpr (P == 2) {
-        const uint2 v = *reinterpret_cast<const uint2*>(p);
-        u[0] = v.x, u[1] = v.y;
-    } else {
-        u[0] = *reinterpret_cast<const uint32_t*>(p);
-    }
-    Chans<P> r;
+__device__ __forceinline__ Chans load_c(const __nv_bfloat16* p) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    const uint32_t u[P] = {v.x, v.y};
+    Chans r;
 #pragma unroll
     for (int i = 0; i < P; ++i)
         r.c[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
     return r;
 }
-template <int P>
-__device__ __forceinline__ Chans<P> load_c(const float* p) {
-    Chans<P> r;
-    if constexpr (P == 2) {
-        const float4 v = *reinterpret_cast<const float4*>(p);
-        r.c[0] = make_float2(v.x, v.y), r.c[1] = make_float2(v.z, v.w);
-    } else {
-        r.c[0] = *reinterpret_cast<const float2*>(p);
-    }
+__device__ __forceinline__ Chans load_c(const float* p) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    Chans r;
+    r.c[0] = make_float2(v.x, v.y), r.c[1] = make_float2(v.z, v.w);
     return r;
 }
-template <int P>
-__device__ __forceinline__ void store_c(__nv_bfloat16* p, const Chans<P>& v) {
-    if constexpr (P == 2)
-        *reinterpret_cast<uint2*>(p) =
-            make_uint2(pack_bf16x2(v.c[0].x, v.c[0].y), pack_bf16x2(v.c[1].x, v.c[1].y));
-    else
-        *reinterpret_cast<uint32_t*>(p) = pack_bf16x2(v.c[0].x, v.c[0].y);
+__device__ __forceinline__ void store_c(__nv_bfloat16* p, const Chans& v) {
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(pack_bf16x2(v.c[0].x, v.c[0].y), pack_bf16x2(v.c[1].x, v.c[1].y));
 }
-template <int P>
-__device__ __forceinline__ void store_c(float* p, const Chans<P>& v) {
-    if constexpr (P == 2)
-        *reinterpret_cast<float4*>(p) = make_float4(v.c[0].x, v.c[0].y, v.c[1].x, v.c[1].y);
-    else
-        *reinterpret_cast<float2*>(p) = v.c[0];
+__device__ __forceinline__ void store_c(float* p, const Chans& v) {
+    *reinterpret_cast<float4*>(p) = make_float4(v.c[0].x, v.c[0].y, v.c[1].x, v.c[1].y);
 }
 
 // What a warp carries from row to row.
-template <int P>
 struct GradState {
-    Chans<P> w[4], dw[4];
-    Chans<P> x1, x2, x3;  // raw rows t - 1, t - 2, t - 3 (zeros before the sequence)
-    Chans<P> d1, d2, d3;  // dx of tokens t - 1, t - 2, t - 3 so far
+    Chans w[4], dw[4];
+    Chans x1, x2, x3;  // raw rows t - 1, t - 2, t - 3 (zeros before the sequence)
+    Chans d1, d2, d3;  // dx of tokens t - 1, t - 2, t - 3 so far
     int lo;               // the first token whose dx is pending or stored here
 };
 
 // Rows t .. t + NR - 1 of one sequence: x and dout at xs, gs (rows `pitch` elements apart);
 // dx of tokens t - 3 .. t + NR - 4 is complete after it and stored.  ALL: every one of them
 // belongs to the run.
-template <int NR, bool L2, bool SILU, bool DW, bool ALL, typename IO, int P>
-__device__ __forceinline__ void grad_rows(GradState<P>& s, int t, const IO* xs, const IO* gs,
+template <int NR, bool L2, bool SILU, bool DW, bool ALL, typename IO>
+__device__ __forceinline__ void grad_rows(GradState& s, int t, const IO* xs, const IO* gs,
                                           int64_t pitch, IO* dx, int64_t rs, float eps) {
-    Chans<P> x[NR + 3], u[NR], slope[NR], dy[NR];
+    Chans x[NR + 3], u[NR], slope[NR], dy[NR];
     x[0] = s.x3, x[1] = s.x2, x[2] = s.x1;
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        x[i + 3] = load_c<P>(xs + i * pitch);
-        dy[i] = load_c<P>(gs + i * pitch);
+        x[i + 3] = load_c(xs + i * pitch);
+        dy[i] = load_c(gs + i * pitch);
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i) {
-        const Chans<P> y = fma_c(
+        const Chans y = fma_c(
             s.w[0], x[i],
             fma_c(s.w[1], x[i + 1], fma_c(s.w[2], x[i + 2], mul_c(s.w[3], x[i + 3]))));
         u[i] = y;
@@ -483,7 +458,7 @@ __device__ __forceinline__ void grad_rows(GradState<P>& s, int t, const IO* xs, 
         if (DW)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s.dw[k] = fma_c(dy[i], x[i + k], s.dw[k]);
-        const Chans<P> done = fma_c(s.w[0], dy[i], s.d3);
+        const Chans done = fma_c(s.w[0], dy[i], s.d3);
         if (ALL || t + i - 3 >= s.lo) store_c(dx + (t + i - 3) * rs, done);
         s.d3 = fma_c(s.w[1], dy[i], s.d2);
         s.d2 = fma_c(s.w[2], dy[i], s.d1);
@@ -493,27 +468,27 @@ __device__ __forceinline__ void grad_rows(GradState<P>& s, int t, const IO* xs, 
 }
 
 // Nothing follows token t - 1 in its sequence or run: what waits is complete.
-template <typename IO, int P>
-__device__ __forceinline__ void grad_flush(const GradState<P>& s, int t, int tb, IO* dx, int64_t rs) {
+template <typename IO>
+__device__ __forceinline__ void grad_flush(const GradState& s, int t, int tb, IO* dx, int64_t rs) {
     if (t - 3 >= s.lo && t - 3 < tb) store_c(dx + (t - 3) * rs, s.d3);
     if (t - 2 >= s.lo && t - 2 < tb) store_c(dx + (t - 2) * rs, s.d2);
     if (t - 1 >= s.lo && t - 1 < tb) store_c(dx + (t - 1) * rs, s.d1);
 }
 
 template <typename IO, bool SILU, bool L2>
-__device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>& s,
+__device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState& s,
                                          const IO* x, const IO* go, IO* dx, int64_t rs, int ta,
                                          int tb, int T_end, const CUtensorMap* mx,
                                          const CUtensorMap* mg, int c0, uint8_t* ring,
                                          uint64_t* full, volatile int* abort_flag) {
-    constexpr int P = 2, ROWS = FG_HALF / (FD * (int)sizeof(IO)), STAGES = FG_STAGES;
+    constexpr int ROWS = FG_HALF / (FD * (int)sizeof(IO)), STAGES = FG_STAGES;
     const int lane = threadIdx.x & 31;
     // (the three tokens ahead of the run's last are read too, for the run's dx alone)
     const int te = min(tb + 3, T_end), tiles = (te - ta + ROWS - 1) / ROWS;
     const auto fetch = [&](int i) {
         if (i >= tiles || lane != 0) return;
         uint8_t* d = ring + (i & (STAGES - 1)) * (2 * FG_HALF);
-        uint64_t* bar = &full[(i & (STAGES - 1))];
+        uint64_t* bar = &full[i & (STAGES - 1)];
         mbar_arrive_expect_tx(bar, 2 * FG_HALF);
         tma_load_2d(d, mx, c0, ta + i * ROWS, bar);
         tma_load_2d(d + FG_HALF, mg, c0, ta + i * ROWS, bar);
@@ -531,14 +506,14 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
         first = max(a.cu_seqlens[n], 0);
         next = a.cu_seqlens[n + 1];
     }
-    s.x1 = ta - 1 >= first ? load_c<P>(x + (ta - 1) * rs) : zeros<P>();
-    s.x2 = ta - 2 >= first ? load_c<P>(x + (ta - 2) * rs) : zeros<P>();
-    s.x3 = ta - 3 >= first ? load_c<P>(x + (ta - 3) * rs) : zeros<P>();
-    s.d1 = s.d2 = s.d3 = zeros<P>();
+    s.x1 = ta - 1 >= first ? load_c(x + (ta - 1) * rs) : zeros();
+    s.x2 = ta - 2 >= first ? load_c(x + (ta - 2) * rs) : zeros();
+    s.x3 = ta - 3 >= first ? load_c(x + (ta - 3) * rs) : zeros();
+    s.d1 = s.d2 = s.d3 = zeros();
     s.lo = max(first, ta);
     const auto start = [&](int t) {  // a sequence starts at token t
         grad_flush(s, t, tb, dx, rs);
-        s.x1 = s.x2 = s.x3 = s.d1 = s.d2 = s.d3 = zeros<P>();
+        s.x1 = s.x2 = s.x3 = s.d1 = s.d2 = s.d3 = zeros();
         s.lo = t;
         do {
             ++n;
@@ -549,11 +524,11 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
     for (int i = 0; i < tiles; ++i) {
         // (the lanes give up together: those that went on would wait for the others in a shuffle)
         if (!__all_sync(0xffffffffu,
-                        mbar_wait(&full[(i & (STAGES - 1))], (i / STAGES) & 1, abort_flag))) {
+                        mbar_wait(&full[i & (STAGES - 1)], (i / STAGES) & 1, abort_flag))) {
             // the copies may still land: wait for them (bounded) before the block ends
             const unsigned long long ts = globaltimer();
             for (int k = i; k < min(i + STAGES - 1, tiles); ++k)
-                while (!mbar_try_wait(smem_u32(&full[(k & (STAGES - 1))]), (k / STAGES) & 1) &&
+                while (!mbar_try_wait(smem_u32(&full[k & (STAGES - 1)]), (k / STAGES) & 1) &&
                        globaltimer() - ts < kWaitLimitNs) {
                 }
             return;
@@ -601,32 +576,29 @@ __device__ __forceinline__ void grad_run(const FrontendGradArgs& a, GradState<2>
 }
 
 template <typename IO, int ACT>
-__global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
+__global__ void __launch_bounds__(32, FG_BLOCKS)
     frontend_grad_kernel(const __grid_constant__ FrontendGradMaps maps, const FrontendGradParams p) {
-    constexpr int P = 2;
     const FrontendGradArgs& a = p.a;
     const int T_end = a.cu_seqlens ? min(max(a.cu_seqlens[a.N], 0), a.T) : a.T;
     extern __shared__ __align__(128) uint8_t fg_sm[];
     allow_next_step();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    uint8_t* ring = fg_sm + warp * FG_RING;
-    uint64_t* full = reinterpret_cast<uint64_t*>(fg_sm + FG_WARPS * FG_RING) + warp * FG_STAGES;
-    volatile int* abort_flag =
-        reinterpret_cast<volatile int*>(fg_sm + FG_WARPS * (FG_RING + FG_STAGES * 8));
-    if (threadIdx.x == 0) *abort_flag = 0;
+    const int lane = threadIdx.x;
+    uint8_t* ring = fg_sm;
+    uint64_t* full = reinterpret_cast<uint64_t*>(fg_sm + FG_RING);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(fg_sm + FG_RING + FG_STAGES * 8);
     if (lane == 0) {
+        *abort_flag = 0;
         for (int i = 0; i < FG_STAGES; ++i) mbar_init(&full[i], 1);
         fence_mbar_init();
     }
-    __syncthreads();
+    __syncwarp();
     // unit: a run of a head, those of q and k first
     const int units_qk = p.qk.runs * 2 * a.H_qk;
-    const int unit = blockIdx.x * FG_WARPS + warp;
+    const int unit = blockIdx.x;
     const bool is_v = unit >= units_qk;
     const GradRuns& runs = is_v ? p.v : p.qk;
     const int heads = is_v ? a.H_v : 2 * a.H_qk;
     const int run = (is_v ? unit - units_qk : unit) / heads;
-    if (run >= runs.runs) return;
     const int head = (is_v ? unit - units_qk : unit) - run * heads;  // among the kind's
     const int hid = is_v ? 2 * a.H_qk + head : head;
     const int kind = hid < a.H_qk ? 0 : (hid < 2 * a.H_qk ? 1 : 2);  // q, k, v
@@ -639,7 +611,7 @@ __global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
     IO* dx = static_cast<IO*>(kind == 0 ? a.dx[0] : (kind == 1 ? a.dx[1] : a.dx[2])) + off;
     const int64_t wc = (int64_t)hid * FD + 4 * lane;  // the lane's channel of the weight
 
-    GradState<P> s;
+    GradState s;
     // the lane's channels x 4 taps, channel-major -> the taps' pairs of channels
     const float4* wp = reinterpret_cast<const float4*>(a.w) + wc;
 #pragma unroll
@@ -651,7 +623,7 @@ __global__ void __launch_bounds__(FG_WARPS * 32, FG_BLOCKS)
         s.w[3].c[c] = make_float2(u.w, v.w);
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) s.dw[k] = zeros<P>();
+    for (int k = 0; k < 4; ++k) s.dw[k] = zeros();
     const int64_t first = (int64_t)run * runs.len;
     const int ta = (int)min(first, (int64_t)T_end), tb = (int)min(first + runs.len, (int64_t)T_end);
     if (ta < tb) {
@@ -708,7 +680,7 @@ __global__ void __launch_bounds__(FG_LAST)
 // the last warps of q and k ran alone: 485 us against 420 us for 32,768 tokens of 16/48 bf16
 // heads).
 void frontend_grad_runs(int T, int H_qk, int H_v, GradRuns& qk, GradRuns& v) {
-    const long long warps = (long long)known_sms() * FG_BLOCKS * FG_WARPS;
+    const long long warps = (long long)known_sms() * FG_BLOCKS;
     const auto cut = [T](long long runs) {
         const long long most = ((long long)T + 31) / 32;
         if (runs > most) runs = most;
@@ -737,9 +709,8 @@ cudaError_t launch_frontend_grad(const FrontendGradParams& p, cudaStream_t strea
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, FG_SMEM);
     if (e != cudaSuccess) return e;
     const long long units = (long long)p.qk.runs * 2 * a.H_qk + (long long)p.v.runs * a.H_v;
-    const long long blocks = (units + FG_WARPS - 1) / FG_WARPS;
     if (units > 0x7fff0000LL) return cudaErrorInvalidConfiguration;
-    kernel<<<(unsigned)blocks, FG_WARPS * 32, FG_SMEM, stream>>>(maps, p);
+    kernel<<<(unsigned)units, 32, FG_SMEM, stream>>>(maps, p);
     return cudaGetLastError();
 }
 
