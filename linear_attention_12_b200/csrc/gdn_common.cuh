@@ -73,16 +73,15 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar_addr, uint32_t parity
 
 // Wait until the phase with the given parity has completed.  Returns false
 // (after recording GDN_DEV_TIMEOUT and raising *abort) when the wait exceeds
-// its limit or another thread of the CTA already aborted.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
-                                          unsigned long long limit = kWaitLimitNs) {
+// kWaitLimitNs or another thread of the CTA already aborted.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort) {
     const uint32_t addr = smem_u32(bar);
     if (mbar_try_wait(addr, parity)) return true;
     const unsigned long long t0 = globaltimer();
     for (;;) {
         if (mbar_try_wait(addr, parity)) return true;
         if (*abort) return false;
-        if (globaltimer() - t0 > limit) {
+        if (globaltimer() - t0 > kWaitLimitNs) {
             atomicOr(&g_status, GDN_DEV_TIMEOUT);
             *abort = 1;
             return false;
