@@ -503,7 +503,8 @@ GDN_API gdn_status gdn_frontend_decode_step(const void *q_raw, const void *k_raw
  *               one), or NULL to skip it.  May alias h0 exactly.
  *
  * The recurrence runs in fp32 and h is rounded once.  No value crosses from one
- * sequence into another, not even an infinity or a NaN.  The result does not
+ * sequence into another, not even an infinity or a NaN; within its sequence an
+ * infinite state may become a NaN.  The result does not
  * depend on timing: the same call gives the same bits.
  * Returns GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED or GDN_ERR_CUDA.
  */

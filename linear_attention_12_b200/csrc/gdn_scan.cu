@@ -713,8 +713,8 @@ cudaError_t launch_tiles(const ScanParams& p, cudaStream_t stream) {
     // A second tile on its way hides the first one's latency.  The gradients' five streams
     // stand more in flight badly: past what the memory system needs it only lengthens the
     // queues, clusters progress unevenly and the last ones run alone.  32,768 x 6144 bf16
-    // gradients took 410 us with 18.9 MB in flight and 339 us with 9.4 MB; the forward with
-    // fp32 gates took 246 us with 18.9 MB and 270 us with 9.4 MB.
+    // gradients took 410 us with 18.9 MB in flight and 339 us with 9.4 MB (344 us now); the forward
+    // with fp32 gates took 246 us with 18.9 MB (242 us now) and 270 us with 9.4 MB.
     const int two = !BWD || !TMA || groups * R * (2ll * SM::DATA) <= (15 << 20);
     return cudaLaunchKernelEx(&cfg, kernel, mx, ml, mh, p, R, two);
 }
@@ -726,7 +726,7 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
                       wide_rows(p.out, p.outs, e) &&
                       (!BWD || (wide_rows(p.h, p.hs, e) && wide_rows(p.dla, p.dlas, ge)));
     // Few channels leave one block an SM or less: larger tiles then, for fewer turns of the
-    // cluster (131,072 x 128 bf16 forward: 217 us against 315 us).
+    // cluster (131,072 x 128 bf16 forward: 217 us against 315 us when this was chosen; 133 us now).
     const bool few = ((long long)p.C + CW - 1) / CW * 8 <= known_sms();
     if (few) {
         // (16 rows a warp do not fit the shared memory where three unaligned fp32 tiles are held)
@@ -737,7 +737,7 @@ cudaError_t launch_types(const ScanParams& p, cudaStream_t stream) {
     // Unaligned tiles always come two at a time; smaller ones then, but for two streams of bf16, so
     // as not to queue (32,768 x 3,001: fp32 gradients 449 us against 1713 us with 16 rows a warp,
     // bf16 gradients 357 us against 709 us, fp32 forward 321 us against 379 us, bf16 forward 272 us
-    // against 250 us).
+    // against 250 us; now, the tensors' ends checked: 461, 368, 308 and 242 us).
     constexpr int ST = BWD || sizeof(IO) + sizeof(G) > 4 ? 8 : 16;
     // (the shared memory of three fp32 tiles leaves room for two blocks an SM: their registers then)
     constexpr int MINB = BWD && sizeof(IO) == 4 ? 2 : 3;
